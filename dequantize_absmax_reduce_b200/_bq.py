@@ -39,6 +39,8 @@ GRAN = {"tensor": BQ_GRAN_TENSOR, "channel": BQ_GRAN_CHANNEL, "group": BQ_GRAN_G
         "column_group": BQ_GRAN_COLUMN_GROUP}
 MODE = {"dynamic": BQ_SCALE_DYNAMIC, "static": BQ_SCALE_STATIC, "from_range": BQ_SCALE_FROM_RANGE}
 ROUND = {"rne": BQ_RNE, "rhaz": BQ_RHAZ}
+ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+SCORE = {"softmax": 0, "sigmoid": 1}
 
 
 class bq_qdesc(C.Structure):
@@ -105,6 +107,15 @@ _SIGS = {
     "bq_nvfp4_concat_rows": [_P, _P, C.c_float, _I64, _P, _P, C.c_float, _I64, _I64, _P, _P,
                              C.POINTER(C.c_float), _P],
     "bq_nvfp4_predequant_to_fp8": [_P, _P, _P, _I64, _I64, _P, _P],
+    "bq_fp8_block_gemm_epilogue": [_P, _P, _I64, _I64, _P, _P, _I64, _P, C.c_int, C.c_int, _P, _P, C.c_int, _P, _P],
+    "bq_gemm_epilogue_backward": [_P, _P, C.c_int, _I64, _I64, C.c_int, _P, _P, _P, _SZ, _P],
+    "bq_moe_route": [_P, C.c_int, _I64, _I32, _P, C.c_int, _I32, _I32, _I32, _I32, _I32, C.c_float, _P, _P, _P],
+    "bq_moe_route_backward": [_P, C.c_int, _I64, _I32, _P, _P, C.c_int, _I32, _I32, C.c_float, _P, _P],
+    "bq_moe_group": [_P, _I64, _I32, _I32, _I32, _P, _P, _P, _P],
+    "bq_moe_combine": [_P, C.c_int, _I64, _I64, _P, _P, _I64, _I32, _P, _P, C.c_int, _P],
+    "bq_moe_combine_backward": [_P, _P, C.c_int, _I64, _I64, _P, _P, _I64, _I32, _P, _P, _P],
+    "bq_fp8_grouped_gemm": [_P, _P, _I64, _I64, _P, _P, _I32, _I64, _P, _P, _I64, _P, C.c_int, C.c_int, _I32, _P,
+                            C.c_int, _P],
 }
 for _name, _args in _SIGS.items():
     _f = getattr(lib, _name)
@@ -120,6 +131,8 @@ lib.bq_quantize_workspace_size.argtypes = [_DESC, C.c_int, _I32, _I64, C.c_int]
 lib.bq_quantize_workspace_size.restype = _SZ
 lib.bq_packed_transpose_stride.argtypes = [_I64, _I64]
 lib.bq_packed_transpose_stride.restype = _I64
+lib.bq_gemm_epilogue_backward_workspace_size.argtypes = [_I64, _I64]
+lib.bq_gemm_epilogue_backward_workspace_size.restype = _SZ
 lib.bq_check_device_error.argtypes = []
 lib.bq_check_device_error.restype = C.c_int
 
@@ -495,3 +508,125 @@ def bq_fp8_tensor_quantize(x, e4m3, scale, static_scale=False, ws=None, stream=N
 def bq_fp8_tensor_dequantize(e4m3, scale, y, stream=None):
     _check(lib.bq_fp8_tensor_dequantize(_ptr(e4m3), _ptr(scale), y.numel(), _ptr(y), DTYPE[y.dtype],
                                         _stream(stream)), "bq_fp8_tensor_dequantize")
+
+
+# ---------------------------------------------------------------- dense epilogue, expert layers
+# These entries take tensors of several shapes that have to fit together, so the
+# binding checks them (ValueError) before it passes bare pointers on, and makes
+# the call on the tensors' device, with that device's current stream by default.
+def _need(t, name: str, shape, dtype=None, like=None):
+    """Pointer of an optional tensor after its checks: shape (None: any size), dtype (one or several), device."""
+    if t is None:
+        return None
+    if len(t.shape) != len(shape):
+        raise ValueError(f"{name}: {len(shape)} dimensions wanted, got shape {tuple(t.shape)}")
+    for a, b in zip(t.shape, shape):
+        if b is not None and a != b:
+            raise ValueError(f"{name}: shape {tuple(shape)} wanted, got {tuple(t.shape)}")
+    if dtype is not None and (t.dtype not in dtype if isinstance(dtype, tuple) else t.dtype != dtype):
+        raise ValueError(f"{name}: dtype {dtype} wanted, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError("bq tensors must be contiguous")
+    if like is not None:
+        if t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    elif t.device.type != "cuda":
+        raise ValueError(f"{name} is on {t.device}: a CUDA tensor is wanted")
+    return t.data_ptr()
+
+
+def _call(fn: str, like, stream, *args) -> None:
+    """lib.fn(*args, stream) on the device of `like`."""
+    here = torch.cuda.current_device()
+    there = like.device.index
+    if here == there:
+        _check(getattr(lib, fn)(*args, _stream(stream)), fn)
+        return
+    with torch.cuda.device(there):
+        _check(getattr(lib, fn)(*args, _stream(stream)), fn)
+
+
+_F = (torch.float32, torch.float16, torch.bfloat16)
+
+
+def bq_fp8_block_gemm_epilogue(a_e4m3, a_scale, w_e4m3, w_scale, c, bias=None, act="none", residual=None,
+                               pre=None, stream=None):
+    m, k = a_e4m3.shape
+    n = w_e4m3.shape[0]
+    nkb = k // 128
+    _call("bq_fp8_block_gemm_epilogue", a_e4m3, stream, _need(a_e4m3, "a_e4m3", (m, k), torch.uint8),
+          _need(a_scale, "a_scale", (m, nkb), torch.float32, a_e4m3), m, k,
+          _need(w_e4m3, "w_e4m3", (n, k), torch.uint8, a_e4m3),
+          _need(w_scale, "w_scale", ((n + 127) // 128, nkb), torch.float32, a_e4m3), n,
+          _need(bias, "bias", (n,), _F, a_e4m3), DTYPE[bias.dtype] if bias is not None else 0, ACT[act],
+          _need(residual, "residual", (m, n), c.dtype, a_e4m3), _need(c, "c", (m, n), None, a_e4m3), DTYPE[c.dtype],
+          _need(pre, "pre", (m, n), c.dtype, a_e4m3))
+
+
+def bq_gemm_epilogue_backward_workspace_size(m: int, n: int) -> int:
+    return int(lib.bq_gemm_epilogue_backward_workspace_size(m, n))
+
+
+def bq_gemm_epilogue_backward(dy, pre, act, dz, dbias=None, ws=None, stream=None):
+    m, n = dy.shape
+    _call("bq_gemm_epilogue_backward", dy, stream, _need(dy, "dy", (m, n)), _need(pre, "pre", (m, n), dy.dtype, dy),
+          DTYPE[dy.dtype], m, n, ACT[act], _need(dz, "dz", (m, n), dy.dtype, dy),
+          _need(dbias, "dbias", (n,), torch.float32, dy), _ptr(ws), _nbytes(ws))
+
+
+def bq_moe_route(logits, bias, score, n_groups, top_groups, group_top, top_k, renormalize, scale, ids, weights,
+                 stream=None):
+    t, e = logits.shape
+    _call("bq_moe_route", logits, stream, _need(logits, "logits", (t, e)), DTYPE[logits.dtype], t, e,
+          _need(bias, "bias", (e,), torch.float32, logits), SCORE[score], n_groups, top_groups, group_top, top_k,
+          int(bool(renormalize)), scale, _need(ids, "ids", (t, top_k), torch.int32, logits),
+          _need(weights, "weights", (t, top_k), torch.float32, logits))
+
+
+def bq_moe_route_backward(logits, ids, dweights, score, renormalize, scale, dlogits, stream=None):
+    t, e = logits.shape
+    top_k = ids.shape[1]
+    _call("bq_moe_route_backward", logits, stream, _need(logits, "logits", (t, e)), DTYPE[logits.dtype], t, e,
+          _need(ids, "ids", (t, top_k), torch.int32, logits),
+          _need(dweights, "dweights", (t, top_k), torch.float32, logits), SCORE[score], top_k,
+          int(bool(renormalize)), scale, _need(dlogits, "dlogits", (t, e), logits.dtype, logits))
+
+
+def bq_moe_group(ids, first_expert, n_experts, offsets, rows, pos, stream=None):
+    t, top_k = ids.shape
+    _call("bq_moe_group", ids, stream, _need(ids, "ids", (t, top_k), torch.int32), t, top_k, first_expert, n_experts,
+          _need(offsets, "offsets", (n_experts + 1,), torch.int32, ids),
+          _need(rows, "rows", (t * top_k,), torch.int32, ids), _need(pos, "pos", (t, top_k), torch.int32, ids))
+
+
+def bq_moe_combine(y, pos, weights, residual, out, stream=None):
+    p, h = y.shape
+    t, top_k = pos.shape
+    _call("bq_moe_combine", y, stream, _need(y, "y", (p, h)), DTYPE[y.dtype], p, h,
+          _need(pos, "pos", (t, top_k), torch.int32, y), _need(weights, "weights", (t, top_k), torch.float32, y),
+          t, top_k, _need(residual, "residual", (t, h), out.dtype, y), _need(out, "out", (t, h), None, y),
+          DTYPE[out.dtype])
+
+
+def bq_moe_combine_backward(dout, y, pos, weights, dy, dweights, stream=None):
+    p, h = y.shape
+    t, top_k = pos.shape
+    _call("bq_moe_combine_backward", y, stream, _need(dout, "dout", (t, h), y.dtype, y), _need(y, "y", (p, h)),
+          DTYPE[y.dtype], p, h, _need(pos, "pos", (t, top_k), torch.int32, y),
+          _need(weights, "weights", (t, top_k), torch.float32, y), t, top_k, _need(dy, "dy", (p, h), y.dtype, y),
+          _need(dweights, "dweights", (t, top_k), torch.float32, y))
+
+
+def bq_fp8_grouped_gemm(a_e4m3, a_scale, rows, offsets, w_e4m3, w_scale, c, bias=None, act="none", gated=False,
+                        stream=None):
+    ar, k = a_e4m3.shape
+    e, n, _ = w_e4m3.shape
+    p = c.shape[0]
+    nkb = k // 128
+    _call("bq_fp8_grouped_gemm", a_e4m3, stream, _need(a_e4m3, "a_e4m3", (ar, k), torch.uint8),
+          _need(a_scale, "a_scale", (ar, nkb), torch.float32, a_e4m3), ar, k,
+          _need(rows, "rows", (p,), torch.int32, a_e4m3), _need(offsets, "offsets", (e + 1,), torch.int32, a_e4m3),
+          e, p, _need(w_e4m3, "w_e4m3", (e, n, k), torch.uint8, a_e4m3),
+          _need(w_scale, "w_scale", (e, (n + 127) // 128, nkb), torch.float32, a_e4m3), n,
+          _need(bias, "bias", (e, n), _F, a_e4m3), DTYPE[bias.dtype] if bias is not None else 0, ACT[act],
+          int(bool(gated)), _need(c, "c", (p, n // 2 if gated else n), None, a_e4m3), DTYPE[c.dtype])

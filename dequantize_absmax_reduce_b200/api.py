@@ -356,3 +356,125 @@ def fp8_tensor_dequantize(e, scale, ydtype=torch.bfloat16, stream=None):
     sc = scale if isinstance(scale, torch.Tensor) else torch.tensor([float(scale)], device=e.device)
     B.bq_fp8_tensor_dequantize(e, sc, y, stream)
     return y
+
+
+# ---------------------------------------------------------------- dense epilogue
+def fp8_block_gemm_epilogue(a_e4m3, a_scale, w_e4m3, w_scale, bias=None, act: str = "none", residual=None,
+                            out_dtype=torch.bfloat16, save_pre: bool = False, stream=None):
+    """act(A @ W^T + bias) + residual from quantized activations (as
+    fp8_block_gemm_quantized takes them), in one kernel and rounded once. act:
+    "none", "relu", "gelu", "gelu_tanh" or "silu"; bias [n] f32 / f16 / bf16;
+    residual [m, n] of out_dtype (f32, f16 or bf16). Returns c [m, n], or (c,
+    pre) with save_pre=True: pre, the value before the activation, is what
+    gemm_epilogue_backward takes."""
+    m, n = a_e4m3.shape[0], w_e4m3.shape[0]
+    c = torch.empty((m, n), dtype=out_dtype, device=a_e4m3.device)
+    pre = torch.empty_like(c) if save_pre else None
+    B.bq_fp8_block_gemm_epilogue(a_e4m3, a_scale, w_e4m3, w_scale, c, bias, act, residual, pre, stream)
+    return (c, pre) if save_pre else c
+
+
+def gemm_epilogue_backward(dy, pre, act: str, bias_grad: bool = True, stream=None):
+    """Gradients of act(pre) with pre = A @ W^T + bias, for dy [m, n]: (dz =
+    dy * act'(pre) in dy's dtype, dbias f32 [n] = its sum over the rows, or
+    None). The gradient of a residual is dy itself."""
+    m, n = dy.shape
+    dz = torch.empty_like(dy)
+    dbias = ws = None
+    if bias_grad:
+        dbias = torch.empty(n, dtype=torch.float32, device=dy.device)
+        ws = torch.empty(B.bq_gemm_epilogue_backward_workspace_size(m, n), dtype=torch.uint8, device=dy.device)
+    B.bq_gemm_epilogue_backward(dy, pre, act, dz, dbias, ws, stream)
+    return dz, dbias
+
+
+# ---------------------------------------------------------------- expert layers
+def moe_route(logits, top_k: int, bias=None, score: str = "softmax", n_groups: int = 1, top_groups: int = 1,
+              group_top: int = 2, renormalize: bool = True, scale: float = 1.0, stream=None):
+    """Experts of each token: logits [t, e] (f32 / f16 / bf16) -> (ids int32
+    [t, top_k] by falling choice value, weights f32 [t, top_k]). Scores are the
+    row's softmax or each logit's sigmoid; `bias` (f32 [e], for the balance of
+    the load) is added for the choice only. With n_groups > 1 the choice is
+    limited to the top_groups groups of consecutive experts whose group_top
+    (1 or 2) best choice values sum highest. Weights are scale * score, divided
+    by the chosen scores' sum with renormalize. Experts at -inf are never
+    chosen: missing ones have id -1 and weight 0."""
+    t = logits.shape[0]
+    ids = torch.empty((t, top_k), dtype=torch.int32, device=logits.device)
+    w = torch.empty((t, top_k), dtype=torch.float32, device=logits.device)
+    B.bq_moe_route(logits, bias, score, n_groups, top_groups, group_top, top_k, renormalize, scale, ids, w, stream)
+    return ids, w
+
+
+def moe_route_backward(logits, ids, dweights, score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                       stream=None):
+    """Gradient of moe_route's weights with respect to the logits, in their
+    dtype (the choice and its bias have none)."""
+    dl = torch.empty_like(logits)
+    B.bq_moe_route_backward(logits, ids, dweights, score, renormalize, scale, dl, stream)
+    return dl
+
+
+def moe_group(ids, n_experts: int, first_expert: int = 0, stream=None):
+    """Expert order of the pairs (token, slot) of ids [t, top_k] whose expert is
+    one of the n_experts from first_expert: (offsets int32 [n_experts + 1], rows
+    int32 [t * top_k]: the token at each position, -1 behind the last, pos int32
+    [t, top_k]: each pair's position, -1 for other experts)."""
+    t, k = ids.shape
+    offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=ids.device)
+    rows = torch.empty(t * k, dtype=torch.int32, device=ids.device)
+    pos = torch.empty((t, k), dtype=torch.int32, device=ids.device)
+    B.bq_moe_group(ids, first_expert, n_experts, offsets, rows, pos, stream)
+    return offsets, rows, pos
+
+
+def moe_combine(y, pos, weights, residual=None, out_dtype=None, stream=None):
+    """out[t] = residual[t] + sum_j weights[t, j] * y[pos[t, j]] (a position
+    outside y adds nothing), in out_dtype (y's unless given; a residual has it
+    too)."""
+    out = torch.empty((pos.shape[0], y.shape[1]), dtype=out_dtype or y.dtype, device=y.device)
+    B.bq_moe_combine(y, pos, weights, residual, out, stream)
+    return out
+
+
+def moe_combine_backward(dout, y, pos, weights, stream=None):
+    """(dy like y, dweights f32 like weights) of moe_combine. Rows of dy that no
+    position names are not written."""
+    dy = torch.empty_like(y)
+    dw = torch.empty_like(weights)
+    B.bq_moe_combine_backward(dout, y, pos, weights, dy, dw, stream)
+    return dy, dw
+
+
+def fp8_grouped_gemm(a_e4m3, a_scale, offsets, w_e4m3, w_scale, rows=None, bias=None, act: str = "none",
+                     gated: bool = False, out_dtype=torch.bfloat16, out=None, stream=None):
+    """Every expert's rows times its weights: position p of expert e (offsets[e]
+    <= p < offsets[e + 1], as moe_group gives them) takes activation row rows[p]
+    (p without rows) of the quantized a_e4m3 / a_scale and gives act(a @
+    w[e]^T + bias[e]), or gated act(z[:, :n/2]) * z[:, n/2:]. w_e4m3 [e, n, k],
+    w_scale [e, ceil(n/128), k/128], bias [e, n]. Returns [positions, n or n/2]
+    (`out` if given); rows behind the last expert's are not written."""
+    if out is None:
+        n = w_e4m3.shape[1]
+        p = a_e4m3.shape[0] if rows is None else rows.shape[0]
+        out = torch.empty((p, n // 2 if gated else n), dtype=out_dtype, device=a_e4m3.device)
+    B.bq_fp8_grouped_gemm(a_e4m3, a_scale, rows, offsets, w_e4m3, w_scale, out, bias, act, gated, stream)
+    return out
+
+
+def fp8_moe(x, logits, w1, w1_scale, w2, w2_scale, top_k: int, bias=None, score: str = "softmax", n_groups: int = 1,
+            top_groups: int = 1, group_top: int = 2, renormalize: bool = True, scale: float = 1.0, act: str = "silu",
+            first_expert: int = 0, residual=None, stream=None):
+    """A whole expert layer in block FP8: residual[t] + sum over the token's
+    experts of weight * ((act(x w1g^T) * (x w1u^T)) w2^T). x [t, h] bf16 / f16,
+    logits [t, experts]; w1 [e, 2 i, h] (the gate's rows first) and w2 [e, h, i]
+    E4M3 codes of the e experts from first_expert (the others' share is left
+    out: with experts spread over GPUs their sums are added up) with 128x128
+    scales. i % 128 == 0 and h % 128 == 0. Returns [t, h] in x's dtype."""
+    ids, w = moe_route(logits, top_k, bias, score, n_groups, top_groups, group_top, renormalize, scale, stream)
+    offsets, rows, pos = moe_group(ids, w1.shape[0], first_expert, stream)
+    ea, sa = fp8_block_quantize(x, 1, 128, stream=stream)
+    h = fp8_grouped_gemm(ea, sa, offsets, w1, w1_scale, rows=rows, act=act, gated=True, out_dtype=x.dtype, stream=stream)
+    eh, sh = fp8_block_quantize(h, 1, 128, stream=stream)
+    y = fp8_grouped_gemm(eh, sh, offsets, w2, w2_scale, out_dtype=x.dtype, stream=stream)
+    return moe_combine(y, pos, w, residual=residual, stream=stream)

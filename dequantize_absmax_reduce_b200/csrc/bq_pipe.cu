@@ -133,12 +133,13 @@ cudaError_t fp8_tensor_quant(DT dt, const void* x, int64_t n, uint8_t* e4m3, flo
 }
 
 cudaError_t pipe_error_take(unsigned int* flag) {
-    unsigned int a = 0, b = 0, c = 0, d = 0;
+    unsigned int a = 0, b = 0, c = 0, d = 0, x = 0;
     cudaError_t e = pipe_err_f32(&a);
     if (e == cudaSuccess) e = pipe_err_f16(&b);
     if (e == cudaSuccess) e = pipe_err_bf16(&c);
     if (e == cudaSuccess) e = gemm_error_take(&d);
-    *flag = a | b | c | d;
+    if (e == cudaSuccess) e = experts_error_take(&x);
+    *flag = a | b | c | d | x;
     return e;
 }
 

@@ -557,6 +557,139 @@ bq_status bq_nvfp4_predequant_to_fp8(const uint8_t* packed, const uint8_t* scale
                                      const float* global_scale, int64_t n, int64_t k,
                                      uint8_t* e4m3, void* stream);
 
+/* ------------------------------------------- dense product with an epilogue */
+/* Activations of the products' epilogues: max(z, 0); z Phi(z); its tanh form
+ * z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))); z / (1 + exp(-z)). */
+typedef enum bq_act {
+    BQ_ACT_NONE = 0, BQ_ACT_RELU = 1, BQ_ACT_GELU = 2, BQ_ACT_GELU_TANH = 3, BQ_ACT_SILU = 4
+} bq_act;
+
+/* The product of bq_fp8_block_gemm_quantized with bias, activation and
+ * residual in its epilogue, all in f32 and rounded once:
+ *   pre[i, j] = P[i, j] + bias[j],  c[i, j] = act(pre[i, j]) + residual[i, j].
+ *   a_e4m3 / a_scale, w_e4m3 / w_scale: as there;
+ *   bias     [n] F32, F16 or BF16 (bias_dtype), or NULL;
+ *   residual [m, n] of c's dtype, 16-byte aligned, or NULL; it may be c;
+ *   c        [m, n] F32, F16 or BF16 (c_dtype), 16-byte aligned, overwritten;
+ *   pre      [m, n] of c's dtype, 16-byte aligned, or NULL: the value before
+ *            the activation, which bq_gemm_epilogue_backward takes.
+ * Shape rules, errors and accuracy of P as there (P + bias, the activation and
+ * the sum with the residual add a few f32 roundings). One launch. */
+bq_status bq_fp8_block_gemm_epilogue(const uint8_t* a_e4m3, const float* a_scale, int64_t m, int64_t k,
+                                     const uint8_t* w_e4m3, const float* w_scale, int64_t n,
+                                     const void* bias, bq_dtype bias_dtype, bq_act act,
+                                     const void* residual, void* c, bq_dtype c_dtype, void* pre,
+                                     void* stream);
+
+/* Gradient of that epilogue. dy, pre, dz [m, n] of one dtype (F32, F16, BF16):
+ *   dz = dy * act'(pre)              (relu's slope at 0 is 0); dz may be dy;
+ *   dbias [n] f32, or NULL: the sum over the rows of dy * act'(pre), before
+ *            dz's rounding, in f32 over a fixed split of the rows: the same
+ *            bits every time;
+ *   ws       scratch of bq_gemm_epilogue_backward_workspace_size(m, n) bytes
+ *            (device, 4-byte aligned) when dbias is given.
+ * The gradient of the residual is dy, that of A dz W (for a W prepared
+ * transposed, [k, n] with 128x128 scales, bq_fp8_block_gemm_quantized on the
+ * 1x128 codes of dz). m = 0 sets dbias to zeros. */
+size_t bq_gemm_epilogue_backward_workspace_size(int64_t m, int64_t n);
+bq_status bq_gemm_epilogue_backward(const void* dy, const void* pre, bq_dtype dtype, int64_t m, int64_t n,
+                                    bq_act act, void* dz, float* dbias, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+/* ------------------------------------------------------------ expert layers */
+/* An expert layer sends every token through the top_k experts that a router
+ * chooses for it: bq_moe_route chooses, bq_moe_group puts the (token, slot)
+ * pairs in expert order, bq_fp8_grouped_gemm multiplies every expert's rows by
+ * its weights, bq_moe_combine sums the experts' rows back into tokens. */
+typedef enum bq_score { BQ_SCORE_SOFTMAX = 0, BQ_SCORE_SIGMOID = 1 } bq_score;
+
+/* Choice of experts. logits [tokens, experts] F32, F16 or BF16. The score s of
+ * an expert is its logit's softmax over the row or its sigmoid; its choice
+ * value v is s + bias (bias f32 [experts], which balances the load and enters
+ * the choice alone), or without a bias the logit itself (the scores' order).
+ * Scores and choice values are those of f64 arithmetic. An expert with a logit
+ * of -inf or NaN, or a choice value of -inf or NaN, is not available.
+ * Experts form n_groups groups of equal size, consecutive; a group's value is
+ * the sum of its group_top (1 or 2) largest available choice values (-inf with
+ * none). The top_groups groups of largest value stay, and of their experts the
+ * top_k of largest choice value are chosen; of equal values the lowest index
+ * goes first, for groups and experts alike.
+ *   ids     int32 [tokens, top_k], by falling choice value; -1 where fewer
+ *           experts are available;
+ *   weights f32 [tokens, top_k] = scale * s / D with D the sum of the chosen
+ *           experts' scores (renormalize) or 1; 0 where the id is -1. A row
+ *           with a NaN logit gets NaN weights, so that it does not go unseen.
+ * A softmax row whose largest logit is +inf gives those experts equal shares.
+ * experts <= 1024, n_groups <= 32 dividing experts, top_k <= 32 and <=
+ * top_groups * experts / n_groups; tokens * top_k < 2^31. */
+bq_status bq_moe_route(const void* logits, bq_dtype dtype, int64_t tokens, int32_t experts,
+                       const float* bias, bq_score score, int32_t n_groups, int32_t top_groups,
+                       int32_t group_top, int32_t top_k, int32_t renormalize, float scale,
+                       int32_t* ids, float* weights, void* stream);
+
+/* Gradient of the weights with respect to the logits (the choice itself and the
+ * bias have none): dlogits [tokens, experts] of the logits' dtype, overwritten
+ * whole; zero for experts that do not enter a weight. ids as bq_moe_route wrote
+ * them (an id outside [0, experts) has no weight; one that stands twice counts
+ * twice), dweights f32 [tokens, top_k]. dlogits must not overlap logits. */
+bq_status bq_moe_route_backward(const void* logits, bq_dtype dtype, int64_t tokens, int32_t experts,
+                                const int32_t* ids, const float* dweights, bq_score score,
+                                int32_t top_k, int32_t renormalize, float scale, void* dlogits,
+                                void* stream);
+
+/* Expert order of the pairs (token, slot): those whose id lies in
+ * [first_expert, first_expert + n_experts) (the experts held here), sorted by
+ * expert, each expert's in the order of the pairs.
+ *   offsets int32 [n_experts + 1]: expert first_expert + i has the positions
+ *           [offsets[i], offsets[i + 1]);
+ *   rows    int32 [tokens * top_k]: the token at each position, -1 behind the
+ *           last expert's;
+ *   pos     int32 [tokens, top_k]: the position of each pair, -1 for other ids.
+ * n_experts <= 1024. One launch of one cluster of CTAs, no workspace, the same
+ * result every time. ids must not overlap the outputs. */
+bq_status bq_moe_group(const int32_t* ids, int64_t tokens, int32_t top_k, int32_t first_expert,
+                       int32_t n_experts, int32_t* offsets, int32_t* rows, int32_t* pos, void* stream);
+
+/* out[t] = residual[t] + sum over slots j of weights[t, j] * y[pos[t, j]], in
+ * f32 in the order of the slots, the residual last, rounded once. y [y_rows,
+ * hidden] (y_dtype F32, F16 or BF16); a pos outside [0, y_rows) adds nothing;
+ * residual [tokens, hidden] of out's dtype, NULL for none; it may be out. */
+bq_status bq_moe_combine(const void* y, bq_dtype y_dtype, int64_t y_rows, int64_t hidden,
+                         const int32_t* pos, const float* weights, int64_t tokens, int32_t top_k,
+                         const void* residual, void* out, bq_dtype out_dtype, void* stream);
+
+/* Its gradients: dy[pos[t, j]] = weights[t, j] * dout[t], dweights[t, j] =
+ * <dout[t], y[pos[t, j]]> (f32; 0 for a pos outside [0, y_rows)). dout, y and
+ * dy of one dtype. Rows of dy that no pos names are left as they were; a
+ * position must not stand twice. top_k <= 32. dy must not overlap dout or y. */
+bq_status bq_moe_combine_backward(const void* dout, const void* y, bq_dtype dtype, int64_t y_rows,
+                                  int64_t hidden, const int32_t* pos, const float* weights,
+                                  int64_t tokens, int32_t top_k, void* dy, float* dweights,
+                                  void* stream);
+
+/* The experts' products in the block-FP8 format of bq_fp8_block_gemm_quantized.
+ * For every expert e and every position p in [offsets[e], offsets[e + 1]):
+ *   z[p, j] = sum over k-blocks b of a_scale[r, b] * w_scale[e, j / 128, b]
+ *             * sum_{k in b} a[r, k] * w[e, j, k]  + bias[e, j],
+ * r = rows[p], or p without rows; c[p] = act(z[p]), or gated:
+ * c[p, j] = act(z[p, j]) * z[p, n/2 + j], j < n/2 (the gate's rows of w first).
+ *   a_e4m3  [a_rows, k] u8, 16-byte aligned; a_scale [a_rows, k/128] f32;
+ *   rows    int32 [c_rows] or NULL (a row outside [0, a_rows) counts as zeros);
+ *   offsets int32 [n_experts + 1], non-decreasing (an expert may have no row;
+ *           positions are bounded by c_rows);
+ *   w_e4m3  [n_experts, n, k] u8, 16-byte aligned; w_scale [n_experts,
+ *           ceil(n/128), k/128] f32;
+ *   bias    [n_experts, n] of bias_dtype F32, F16 or BF16, or NULL;
+ *   c       [c_rows, n or n/2] F32, F16 or BF16, 16-byte aligned. Rows outside
+ *           every expert's range are left as they were.
+ * k % 128 == 0; gated: n % 256 == 0; n_experts <= 1024; a_rows, c_rows and
+ * n_experts * n < 2^31. Accuracy as for the dense products. One launch. */
+bq_status bq_fp8_grouped_gemm(const uint8_t* a_e4m3, const float* a_scale, int64_t a_rows, int64_t k,
+                              const int32_t* rows, const int32_t* offsets, int32_t n_experts,
+                              int64_t c_rows, const uint8_t* w_e4m3, const float* w_scale, int64_t n,
+                              const void* bias, bq_dtype bias_dtype, bq_act act, int32_t gated,
+                              void* c, bq_dtype c_dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
