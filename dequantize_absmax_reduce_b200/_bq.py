@@ -514,39 +514,43 @@ def bq_fp8_tensor_dequantize(e4m3, scale, y, stream=None):
 # These entries take tensors of several shapes that have to fit together, so the
 # binding checks them (ValueError) before it passes bare pointers on, and makes
 # the call on the tensors' device, with that device's current stream by default.
-def _need(t, name: str, shape, dtype=None, like=None):
-    """Pointer of an optional tensor after its checks: shape (None: any size), dtype (one or several), device."""
+# The checks stand in the way of every call of a few microseconds: one
+# comparison each where a tensor is what is wanted.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+
+
+def _need(t, name: str, shape, dtypes, dev: int):
+    """Pointer of an optional tensor after its checks: shape, dtype (one of `dtypes`), contiguous, on GPU `dev`."""
     if t is None:
         return None
-    if len(t.shape) != len(shape):
-        raise ValueError(f"{name}: {len(shape)} dimensions wanted, got shape {tuple(t.shape)}")
-    for a, b in zip(t.shape, shape):
-        if b is not None and a != b:
-            raise ValueError(f"{name}: shape {tuple(shape)} wanted, got {tuple(t.shape)}")
-    if dtype is not None and (t.dtype not in dtype if isinstance(dtype, tuple) else t.dtype != dtype):
-        raise ValueError(f"{name}: dtype {dtype} wanted, got {t.dtype}")
+    if t.shape == shape and t.dtype in dtypes and t.get_device() == dev >= 0 and t.is_contiguous():
+        return t.data_ptr()
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(shape)} wanted, got {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {' or '.join(map(str, dtypes))} wanted, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError("bq tensors must be contiguous")
-    if like is not None:
-        if t.device != like.device:
-            raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    elif t.device.type != "cuda":
+    if t.device.type != "cuda":
         raise ValueError(f"{name} is on {t.device}: a CUDA tensor is wanted")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, the first tensor on cuda:{dev}")
 
 
-def _call(fn: str, like, stream, *args) -> None:
-    """lib.fn(*args, stream) on the device of `like`."""
-    here = torch.cuda.current_device()
-    there = like.device.index
-    if here == there:
-        _check(getattr(lib, fn)(*args, _stream(stream)), fn)
-        return
-    with torch.cuda.device(there):
-        _check(getattr(lib, fn)(*args, _stream(stream)), fn)
+def _call(fn: str, dev: int, stream, *args) -> None:
+    """lib.fn(*args, stream) on GPU `dev`."""
+    if dev == torch.cuda.current_device():
+        if stream is None and _raw_stream is not None:
+            stream = _raw_stream(dev)
+        status = getattr(lib, fn)(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(lib, fn)(*args, _stream(stream))
+    if status != BQ_OK:
+        raise BqError(status, fn)
 
 
 _F = (torch.float32, torch.float16, torch.bfloat16)
+_F32, _I32T, _U8T = (torch.float32,), (torch.int32,), (torch.uint8,)
 
 
 def bq_fp8_block_gemm_epilogue(a_e4m3, a_scale, w_e4m3, w_scale, c, bias=None, act="none", residual=None,
@@ -554,13 +558,12 @@ def bq_fp8_block_gemm_epilogue(a_e4m3, a_scale, w_e4m3, w_scale, c, bias=None, a
     m, k = a_e4m3.shape
     n = w_e4m3.shape[0]
     nkb = k // 128
-    _call("bq_fp8_block_gemm_epilogue", a_e4m3, stream, _need(a_e4m3, "a_e4m3", (m, k), torch.uint8),
-          _need(a_scale, "a_scale", (m, nkb), torch.float32, a_e4m3), m, k,
-          _need(w_e4m3, "w_e4m3", (n, k), torch.uint8, a_e4m3),
-          _need(w_scale, "w_scale", ((n + 127) // 128, nkb), torch.float32, a_e4m3), n,
-          _need(bias, "bias", (n,), _F, a_e4m3), DTYPE[bias.dtype] if bias is not None else 0, ACT[act],
-          _need(residual, "residual", (m, n), c.dtype, a_e4m3), _need(c, "c", (m, n), None, a_e4m3), DTYPE[c.dtype],
-          _need(pre, "pre", (m, n), c.dtype, a_e4m3))
+    dev, out = a_e4m3.get_device(), (c.dtype,)
+    _call("bq_fp8_block_gemm_epilogue", dev, stream, _need(a_e4m3, "a_e4m3", (m, k), _U8T, dev),
+          _need(a_scale, "a_scale", (m, nkb), _F32, dev), m, k, _need(w_e4m3, "w_e4m3", (n, k), _U8T, dev),
+          _need(w_scale, "w_scale", ((n + 127) // 128, nkb), _F32, dev), n, _need(bias, "bias", (n,), _F, dev),
+          DTYPE[bias.dtype] if bias is not None else 0, ACT[act], _need(residual, "residual", (m, n), out, dev),
+          _need(c, "c", (m, n), _F, dev), DTYPE[c.dtype], _need(pre, "pre", (m, n), out, dev))
 
 
 def bq_gemm_epilogue_backward_workspace_size(m: int, n: int) -> int:
@@ -569,52 +572,56 @@ def bq_gemm_epilogue_backward_workspace_size(m: int, n: int) -> int:
 
 def bq_gemm_epilogue_backward(dy, pre, act, dz, dbias=None, ws=None, stream=None):
     m, n = dy.shape
-    _call("bq_gemm_epilogue_backward", dy, stream, _need(dy, "dy", (m, n)), _need(pre, "pre", (m, n), dy.dtype, dy),
-          DTYPE[dy.dtype], m, n, ACT[act], _need(dz, "dz", (m, n), dy.dtype, dy),
-          _need(dbias, "dbias", (n,), torch.float32, dy), _ptr(ws), _nbytes(ws))
+    dev, dt = dy.get_device(), (dy.dtype,)
+    _call("bq_gemm_epilogue_backward", dev, stream, _need(dy, "dy", (m, n), _F, dev), _need(pre, "pre", (m, n), dt, dev),
+          DTYPE[dy.dtype], m, n, ACT[act], _need(dz, "dz", (m, n), dt, dev), _need(dbias, "dbias", (n,), _F32, dev),
+          _need(ws, "ws", (0 if ws is None else ws.numel(),), _U8T, dev), _nbytes(ws))
 
 
 def bq_moe_route(logits, bias, score, n_groups, top_groups, group_top, top_k, renormalize, scale, ids, weights,
                  stream=None):
     t, e = logits.shape
-    _call("bq_moe_route", logits, stream, _need(logits, "logits", (t, e)), DTYPE[logits.dtype], t, e,
-          _need(bias, "bias", (e,), torch.float32, logits), SCORE[score], n_groups, top_groups, group_top, top_k,
-          int(bool(renormalize)), scale, _need(ids, "ids", (t, top_k), torch.int32, logits),
-          _need(weights, "weights", (t, top_k), torch.float32, logits))
+    dev = logits.get_device()
+    _call("bq_moe_route", dev, stream, _need(logits, "logits", (t, e), _F, dev), DTYPE[logits.dtype], t, e,
+          _need(bias, "bias", (e,), _F32, dev), SCORE[score], n_groups, top_groups, group_top, top_k,
+          1 if renormalize else 0, scale, _need(ids, "ids", (t, top_k), _I32T, dev),
+          _need(weights, "weights", (t, top_k), _F32, dev))
 
 
 def bq_moe_route_backward(logits, ids, dweights, score, renormalize, scale, dlogits, stream=None):
     t, e = logits.shape
     top_k = ids.shape[1]
-    _call("bq_moe_route_backward", logits, stream, _need(logits, "logits", (t, e)), DTYPE[logits.dtype], t, e,
-          _need(ids, "ids", (t, top_k), torch.int32, logits),
-          _need(dweights, "dweights", (t, top_k), torch.float32, logits), SCORE[score], top_k,
-          int(bool(renormalize)), scale, _need(dlogits, "dlogits", (t, e), logits.dtype, logits))
+    dev = logits.get_device()
+    _call("bq_moe_route_backward", dev, stream, _need(logits, "logits", (t, e), _F, dev), DTYPE[logits.dtype], t, e,
+          _need(ids, "ids", (t, top_k), _I32T, dev), _need(dweights, "dweights", (t, top_k), _F32, dev), SCORE[score],
+          top_k, 1 if renormalize else 0, scale, _need(dlogits, "dlogits", (t, e), (logits.dtype,), dev))
 
 
 def bq_moe_group(ids, first_expert, n_experts, offsets, rows, pos, stream=None):
     t, top_k = ids.shape
-    _call("bq_moe_group", ids, stream, _need(ids, "ids", (t, top_k), torch.int32), t, top_k, first_expert, n_experts,
-          _need(offsets, "offsets", (n_experts + 1,), torch.int32, ids),
-          _need(rows, "rows", (t * top_k,), torch.int32, ids), _need(pos, "pos", (t, top_k), torch.int32, ids))
+    dev = ids.get_device()
+    _call("bq_moe_group", dev, stream, _need(ids, "ids", (t, top_k), _I32T, dev), t, top_k, first_expert, n_experts,
+          _need(offsets, "offsets", (n_experts + 1,), _I32T, dev), _need(rows, "rows", (t * top_k,), _I32T, dev),
+          _need(pos, "pos", (t, top_k), _I32T, dev))
 
 
 def bq_moe_combine(y, pos, weights, residual, out, stream=None):
     p, h = y.shape
     t, top_k = pos.shape
-    _call("bq_moe_combine", y, stream, _need(y, "y", (p, h)), DTYPE[y.dtype], p, h,
-          _need(pos, "pos", (t, top_k), torch.int32, y), _need(weights, "weights", (t, top_k), torch.float32, y),
-          t, top_k, _need(residual, "residual", (t, h), out.dtype, y), _need(out, "out", (t, h), None, y),
-          DTYPE[out.dtype])
+    dev = y.get_device()
+    _call("bq_moe_combine", dev, stream, _need(y, "y", (p, h), _F, dev), DTYPE[y.dtype], p, h,
+          _need(pos, "pos", (t, top_k), _I32T, dev), _need(weights, "weights", (t, top_k), _F32, dev), t, top_k,
+          _need(residual, "residual", (t, h), (out.dtype,), dev), _need(out, "out", (t, h), _F, dev), DTYPE[out.dtype])
 
 
 def bq_moe_combine_backward(dout, y, pos, weights, dy, dweights, stream=None):
     p, h = y.shape
     t, top_k = pos.shape
-    _call("bq_moe_combine_backward", y, stream, _need(dout, "dout", (t, h), y.dtype, y), _need(y, "y", (p, h)),
-          DTYPE[y.dtype], p, h, _need(pos, "pos", (t, top_k), torch.int32, y),
-          _need(weights, "weights", (t, top_k), torch.float32, y), t, top_k, _need(dy, "dy", (p, h), y.dtype, y),
-          _need(dweights, "dweights", (t, top_k), torch.float32, y))
+    dev, dt = y.get_device(), (y.dtype,)
+    _call("bq_moe_combine_backward", dev, stream, _need(dout, "dout", (t, h), dt, dev), _need(y, "y", (p, h), _F, dev),
+          DTYPE[y.dtype], p, h, _need(pos, "pos", (t, top_k), _I32T, dev),
+          _need(weights, "weights", (t, top_k), _F32, dev), t, top_k, _need(dy, "dy", (p, h), dt, dev),
+          _need(dweights, "dweights", (t, top_k), _F32, dev))
 
 
 def bq_fp8_grouped_gemm(a_e4m3, a_scale, rows, offsets, w_e4m3, w_scale, c, bias=None, act="none", gated=False,
@@ -623,10 +630,10 @@ def bq_fp8_grouped_gemm(a_e4m3, a_scale, rows, offsets, w_e4m3, w_scale, c, bias
     e, n, _ = w_e4m3.shape
     p = c.shape[0]
     nkb = k // 128
-    _call("bq_fp8_grouped_gemm", a_e4m3, stream, _need(a_e4m3, "a_e4m3", (ar, k), torch.uint8),
-          _need(a_scale, "a_scale", (ar, nkb), torch.float32, a_e4m3), ar, k,
-          _need(rows, "rows", (p,), torch.int32, a_e4m3), _need(offsets, "offsets", (e + 1,), torch.int32, a_e4m3),
-          e, p, _need(w_e4m3, "w_e4m3", (e, n, k), torch.uint8, a_e4m3),
-          _need(w_scale, "w_scale", (e, (n + 127) // 128, nkb), torch.float32, a_e4m3), n,
-          _need(bias, "bias", (e, n), _F, a_e4m3), DTYPE[bias.dtype] if bias is not None else 0, ACT[act],
-          int(bool(gated)), _need(c, "c", (p, n // 2 if gated else n), None, a_e4m3), DTYPE[c.dtype])
+    dev = a_e4m3.get_device()
+    _call("bq_fp8_grouped_gemm", dev, stream, _need(a_e4m3, "a_e4m3", (ar, k), _U8T, dev),
+          _need(a_scale, "a_scale", (ar, nkb), _F32, dev), ar, k, _need(rows, "rows", (p,), _I32T, dev),
+          _need(offsets, "offsets", (e + 1,), _I32T, dev), e, p, _need(w_e4m3, "w_e4m3", (e, n, k), _U8T, dev),
+          _need(w_scale, "w_scale", (e, (n + 127) // 128, nkb), _F32, dev), n, _need(bias, "bias", (e, n), _F, dev),
+          DTYPE[bias.dtype] if bias is not None else 0, ACT[act], 1 if gated else 0,
+          _need(c, "c", (p, n // 2 if gated else n), _F, dev), DTYPE[c.dtype])

@@ -400,8 +400,8 @@ def moe_route(logits, top_k: int, bias=None, score: str = "softmax", n_groups: i
     by the chosen scores' sum with renormalize. Experts at -inf are never
     chosen: missing ones have id -1 and weight 0."""
     t = logits.shape[0]
-    ids = torch.empty((t, top_k), dtype=torch.int32, device=logits.device)
-    w = torch.empty((t, top_k), dtype=torch.float32, device=logits.device)
+    ids = logits.new_empty((t, top_k), dtype=torch.int32)
+    w = logits.new_empty((t, top_k), dtype=torch.float32)
     B.bq_moe_route(logits, bias, score, n_groups, top_groups, group_top, top_k, renormalize, scale, ids, w, stream)
     return ids, w
 
@@ -421,9 +421,9 @@ def moe_group(ids, n_experts: int, first_expert: int = 0, stream=None):
     int32 [t * top_k]: the token at each position, -1 behind the last, pos int32
     [t, top_k]: each pair's position, -1 for other experts)."""
     t, k = ids.shape
-    offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=ids.device)
-    rows = torch.empty(t * k, dtype=torch.int32, device=ids.device)
-    pos = torch.empty((t, k), dtype=torch.int32, device=ids.device)
+    offsets = ids.new_empty(n_experts + 1, dtype=torch.int32)
+    rows = ids.new_empty(t * k, dtype=torch.int32)
+    pos = ids.new_empty((t, k), dtype=torch.int32)
     B.bq_moe_group(ids, first_expert, n_experts, offsets, rows, pos, stream)
     return offsets, rows, pos
 
@@ -471,10 +471,11 @@ def fp8_moe(x, logits, w1, w1_scale, w2, w2_scale, top_k: int, bias=None, score:
     E4M3 codes of the e experts from first_expert (the others' share is left
     out: with experts spread over GPUs their sums are added up) with 128x128
     scales. i % 128 == 0 and h % 128 == 0. Returns [t, h] in x's dtype."""
-    ids, w = moe_route(logits, top_k, bias, score, n_groups, top_groups, group_top, renormalize, scale, stream)
-    offsets, rows, pos = moe_group(ids, w1.shape[0], first_expert, stream)
-    ea, sa = fp8_block_quantize(x, 1, 128, stream=stream)
-    h = fp8_grouped_gemm(ea, sa, offsets, w1, w1_scale, rows=rows, act=act, gated=True, out_dtype=x.dtype, stream=stream)
-    eh, sh = fp8_block_quantize(h, 1, 128, stream=stream)
-    y = fp8_grouped_gemm(eh, sh, offsets, w2, w2_scale, out_dtype=x.dtype, stream=stream)
-    return moe_combine(y, pos, w, residual=residual, stream=stream)
+    with torch.cuda.device(x.device):
+        ids, w = moe_route(logits, top_k, bias, score, n_groups, top_groups, group_top, renormalize, scale, stream)
+        offsets, rows, pos = moe_group(ids, w1.shape[0], first_expert, stream)
+        ea, sa = fp8_block_quantize(x, 1, 128, stream=stream)
+        h = fp8_grouped_gemm(ea, sa, offsets, w1, w1_scale, rows, None, act, True, x.dtype, stream=stream)
+        eh, sh = fp8_block_quantize(h, 1, 128, stream=stream)
+        y = fp8_grouped_gemm(eh, sh, offsets, w2, w2_scale, out_dtype=x.dtype, stream=stream)
+        return moe_combine(y, pos, w, residual=residual, stream=stream)

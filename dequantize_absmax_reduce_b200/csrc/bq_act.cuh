@@ -14,7 +14,12 @@
 
 namespace bq {
 
-__device__ __forceinline__ float logistic(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+__device__ __forceinline__ float logistic(float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));   // exp(-x) = 2^(-x log2 e)
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
 
 constexpr float kGeluA = 0.7978845608028654f;        // sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;

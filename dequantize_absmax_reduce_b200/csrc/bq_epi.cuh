@@ -2,11 +2,12 @@
 // the conversion of a tile's f32 sums, a warp's 32 rows x 32 columns at a time.
 //
 // A promotion thread holds one row of the tile, so writing from its registers
-// would touch 32 rows with every instruction. The 32 x 32 block goes through
-// 4 KB of shared memory instead (16-byte slots swizzled by row: no bank
-// conflicts either way) and comes back with eight lanes along a row, so that
-// bias, residual and results are read and written in whole sectors, and the
-// activation's code stands once per chunk instead of once per register.
+// would touch 32 rows with every instruction. The columns go through shared memory
+// instead (16-byte slots swizzled by row) and come back with four lanes along a
+// row, eight columns each, so that residual and results are read and written in
+// whole sectors with 16-byte accesses. A lane has four rows (gated: one) in flight at
+// once: with two warps per scheduler the activation's chain of instructions would
+// otherwise be waited for row by row.
 #pragma once
 
 #include "bq.h"
@@ -24,115 +25,245 @@ struct EpiArgs {
     int64_t n;              // columns of the product
     int64_t n_out;          // columns of c: n, gated n / 2
     int bias_t, c_t, act;
-    int vec;                // n_out a multiple of 4: vectors of four columns
+    int vec;                // n_out a multiple of 8: vectors of eight columns
+    int bias_vec;           // the same of the bias, which also starts on 16 bytes
 };
-constexpr uint32_t EPI_WARP_BYTES = 32 * 32 * 4;
+[[maybe_unused]] EpiArgs make_epi(int64_t n, int64_t n_out, const void* bias, int bias_t, int act, const void* residual, void* c,
+                                  int c_t, void* pre) {
+    EpiArgs g = {};
+    g.bias = bias; g.residual = residual; g.c = c; g.pre = pre;
+    g.n = n; g.n_out = n_out;
+    g.bias_t = bias_t; g.c_t = c_t; g.act = act;
+    g.vec = n_out % 8 == 0;
+    g.bias_vec = n % 8 == 0 && ((uintptr_t)bias & 15u) == 0;
+    return g;
+}
 
 __device__ __forceinline__ float epi_load(const void* p, int t, int64_t i) {
     if (t == BQ_F32) return reinterpret_cast<const float*>(p)[i];
     if (t == BQ_F16) return __half2float(reinterpret_cast<const __half*>(p)[i]);
     return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
 }
-// Four columns from element i of a row; `left` of them exist.
-__device__ __forceinline__ void epi_load4(const void* p, int t, int64_t i, int left, int vec, float (&v)[4]) {
-    if (vec) {
-        if (t == BQ_F32) {
-            const float4 f = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
-            v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-        } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + i);
-            if (t == BQ_F16) { unpack_f16x2(u.x, v[0], v[1]); unpack_f16x2(u.y, v[2], v[3]); }
-            else { unpack_bf16x2(u.x, v[0], v[1]); unpack_bf16x2(u.y, v[2], v[3]); }
-        }
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = j < left ? epi_load(p, t, i + j) : 0.0f;
-}
-__device__ __forceinline__ void epi_store4(void* p, int t, int64_t i, int left, int vec, const float (&v)[4]) {
-    if (vec) {
-        if (t == BQ_F32)
-            *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
-        else
-            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p) + i) =
-                t == BQ_F16 ? make_uint2(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]))
-                            : make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (j >= left) break;
-        if (t == BQ_F32) reinterpret_cast<float*>(p)[i + j] = v[j];
-        else if (t == BQ_F16) reinterpret_cast<__half*>(p)[i + j] = __float2half_rn(v[j]);
-        else reinterpret_cast<__nv_bfloat16*>(p)[i + j] = __float2bfloat16_rn(v[j]);
+// Eight columns from element i of a row (16-byte aligned).
+__device__ __forceinline__ void epi_load8(const void* p, int t, int64_t i, U4 (&u)[2]) {
+    if (t == BQ_F32) {
+        u[0] = *reinterpret_cast<const U4*>(reinterpret_cast<const float*>(p) + i);
+        u[1] = *reinterpret_cast<const U4*>(reinterpret_cast<const float*>(p) + i + 4);
+    } else {
+        u[0] = *reinterpret_cast<const U4*>(reinterpret_cast<const uint16_t*>(p) + i);
     }
 }
-__device__ __forceinline__ void epi_act4(int act, float (&z)[4]) {
+__device__ __forceinline__ void epi_add8(int t, const U4 (&u)[2], float (&v)[8]) {
+    float r[8];
+    if (t == BQ_F32) {
+        float a[4], b[4];
+        unpack(u[0], a);
+        unpack(u[1], b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) { r[j] = a[j]; r[4 + j] = b[j]; }
+    } else if (t == BQ_F16) {
+        unpack8<__half>(u[0], r);
+    } else {
+        unpack8<__nv_bfloat16>(u[0], r);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += r[j];
+}
+// The biases of eight columns.
+__device__ __forceinline__ void epi_bias8(const EpiArgs& g, int64_t i, float (&v)[8]) {
+    if (g.bias_vec) {
+        U4 u[2];
+        epi_load8(g.bias, g.bias_t, i, u);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+        epi_add8(g.bias_t, u, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = epi_load(g.bias, g.bias_t, i + k);
+    }
+}
+__device__ __forceinline__ void epi_store8(void* p, int t, int64_t i, const float (&v)[8]) {
+    if (t == BQ_F32) {
+        float a[4], b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) { a[j] = v[j]; b[j] = v[4 + j]; }
+        st16(reinterpret_cast<float*>(p) + i, pack_vec<float>(a));
+        st16(reinterpret_cast<float*>(p) + i + 4, pack_vec<float>(b));
+    } else if (t == BQ_F16) {
+        st16(reinterpret_cast<__half*>(p) + i, pack_vec<__half>(v));
+    } else {
+        st16(reinterpret_cast<__nv_bfloat16*>(p) + i, pack_vec<__nv_bfloat16>(v));
+    }
+}
+__device__ __forceinline__ void epi_store(void* p, int t, int64_t i, float v) {
+    if (t == BQ_F32) reinterpret_cast<float*>(p)[i] = v;
+    else if (t == BQ_F16) reinterpret_cast<__half*>(p)[i] = __float2half_rn(v);
+    else reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+template <int ACT, int N>
+__device__ __forceinline__ void act_all(float (&z)[N][8]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[i][j] = act_value<ACT>(z[i][j]);
+}
+template <int N>
+__device__ __forceinline__ void epi_act(int act, float (&z)[N][8]) {
     switch (act) {
-        case BQ_ACT_RELU:
-#pragma unroll
-            for (int j = 0; j < 4; ++j) z[j] = act_value<BQ_ACT_RELU>(z[j]);
-            break;
-        case BQ_ACT_GELU:
-#pragma unroll
-            for (int j = 0; j < 4; ++j) z[j] = act_value<BQ_ACT_GELU>(z[j]);
-            break;
-        case BQ_ACT_GELU_TANH:
-#pragma unroll
-            for (int j = 0; j < 4; ++j) z[j] = act_value<BQ_ACT_GELU_TANH>(z[j]);
-            break;
-        case BQ_ACT_SILU:
-#pragma unroll
-            for (int j = 0; j < 4; ++j) z[j] = act_value<BQ_ACT_SILU>(z[j]);
-            break;
+        case BQ_ACT_RELU: act_all<BQ_ACT_RELU>(z); break;
+        case BQ_ACT_GELU: act_all<BQ_ACT_GELU>(z); break;
+        case BQ_ACT_GELU_TANH: act_all<BQ_ACT_GELU_TANH>(z); break;
+        case BQ_ACT_SILU: act_all<BQ_ACT_SILU>(z); break;
         default: break;
     }
 }
+__device__ __forceinline__ float epi_act1(int act, float z) {
+    switch (act) {
+        case BQ_ACT_RELU: return act_value<BQ_ACT_RELU>(z);
+        case BQ_ACT_GELU: return act_value<BQ_ACT_GELU>(z);
+        case BQ_ACT_GELU_TANH: return act_value<BQ_ACT_GELU_TANH>(z);
+        case BQ_ACT_SILU: return act_value<BQ_ACT_SILU>(z);
+        default: return z;
+    }
+}
 
-// One chunk of a warp: v holds this lane's row (row0 + lane of c). Plain: the
-// columns col .. col + 31. Gated: the gate's columns col .. col + 15, then the
-// other half's. `rows` of the 32 rows exist. bias_at: the first column's place
-// in the bias array.
-template <bool GATED>
-__device__ __forceinline__ void epi_chunk(const EpiArgs& g, float* stage, int lane, int64_t row0, int rows, int64_t col,
-                                          int64_t bias_at, const float (&v)[32]) {
-    if (col >= g.n_out) return;                     // uniform over the warp
-    float4* st = reinterpret_cast<float4*>(stage);
+// This lane's values (row `lane`) into the warp's staging block of ROW4 16-byte
+// slots a row, from slot `first` on: the low three bits of a slot's number are
+// xored with the row's. Zeros for a row without activations.
+template <int ROW4, int N>
+__device__ __forceinline__ void epi_stage(float* stage, int lane, bool row_in, int first, const F2 (&v)[N], int from, int count) {
+    float4* st = reinterpret_cast<float4*>(stage) + lane * ROW4;
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-        st[lane * 8 + (c ^ (lane & 7))] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-    __syncwarp();
-    constexpr int LANES = GATED ? 4 : 8;            // lanes along a row
-    const int c = lane % LANES;
-    const int64_t j = col + 4 * c;
-    const int left = (int)min((int64_t)4, g.n_out - j);
-    if (left > 0) {
-        const int vec = g.vec;
-        float b0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (g.bias) {
-            epi_load4(g.bias, g.bias_t, bias_at + 4 * c, left, 0, b0);
-            if (GATED) epi_load4(g.bias, g.bias_t, bias_at + g.n_out + 4 * c, left, 0, b1);
-        }
-#pragma unroll 2
-        for (int r = lane / LANES; r < rows; r += 32 / LANES) {
-            const int64_t at = (row0 + r) * g.n_out + j;
-            const float4 f = st[r * 8 + (c ^ (r & 7))];
-            float z[4] = {f.x + b0[0], f.y + b0[1], f.z + b0[2], f.w + b0[3]};
-            float res[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (!GATED && g.residual) epi_load4(g.residual, g.c_t, at, left, vec, res);
-            if (!GATED && g.pre) epi_store4(g.pre, g.c_t, at, left, vec, z);
-            epi_act4(g.act, z);
-            if (GATED) {
-                const float4 u = st[r * 8 + ((c + 4) ^ (r & 7))];
-                z[0] *= u.x + b1[0]; z[1] *= u.y + b1[1]; z[2] *= u.z + b1[2]; z[3] *= u.w + b1[3];
-            } else {
+    for (int c = 0; c < N / 2; ++c) {
+        if (c >= count / 4) break;
+        float4 f;
+        f2_split(v[from + 2 * c], f.x, f.y);
+        f2_split(v[from + 2 * c + 1], f.z, f.w);
+        if (!row_in) f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        st[(first + c) ^ (lane & 7)] = f;
+    }
+}
+
+// One staged chunk of a warp, whose rows are row0 + 0 .. of c, `rows` of them.
+// Plain: the columns col .. col + 31. Gated: the gate's columns col .. col + 15,
+// then the other half's. bias_at: the place of column col in the bias array.
+// Rows of the staging block are ROW4 16-byte slots apart; a lane has ROWS rows in
+// flight, as its registers allow.
+template <bool GATED, int ROWS, int ROW4 = 8>
+__device__ __forceinline__ void epi_chunk(const EpiArgs& g, const float* stage, int lane, int64_t row0, int rows, int64_t col,
+                                          int64_t bias_at) {
+    const float4* st = reinterpret_cast<const float4*>(stage);
+    // Lanes along a row; ROWS rows of a lane at a time.
+    constexpr int LANES = GATED ? 2 : 4, RSTEP = 32 / LANES, N = ROWS;
+    if (g.vec && (GATED || col + 32 <= g.n_out)) {
+        const int c = lane % LANES;
+        const int64_t j = col + 8 * c;
+#pragma unroll 1
+        for (int r0 = lane / LANES; r0 < rows; r0 += N * RSTEP) {
+            U4 res[N][2];
+            if (!GATED && g.residual) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) z[i] += res[i];
+                for (int i = 0; i < N; ++i)
+                    if (r0 + i * RSTEP < rows) epi_load8(g.residual, g.c_t, (row0 + r0 + i * RSTEP) * g.n_out + j, res[i]);
             }
-            epi_store4(g.c, g.c_t, at, left, vec, z);
+            float z[N][8], u[GATED ? N : 1][8];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int r = r0 + i * RSTEP;
+                const float4 a = st[r * ROW4 + ((2 * c) ^ (r & 7))], b = st[r * ROW4 + ((2 * c + 1) ^ (r & 7))];
+                z[i][0] = a.x; z[i][1] = a.y; z[i][2] = a.z; z[i][3] = a.w;
+                z[i][4] = b.x; z[i][5] = b.y; z[i][6] = b.z; z[i][7] = b.w;
+                if constexpr (GATED) {
+                    const float4 d = st[r * ROW4 + ((4 + 2 * c) ^ (r & 7))], e = st[r * ROW4 + ((5 + 2 * c) ^ (r & 7))];
+                    u[i][0] = d.x; u[i][1] = d.y; u[i][2] = d.z; u[i][3] = d.w;
+                    u[i][4] = e.x; u[i][5] = e.y; u[i][6] = e.z; u[i][7] = e.w;
+                }
+            }
+            if (g.bias) {
+                if constexpr (GATED) {
+                    // One by one: vectors of both halves' biases beside the sums not
+                    // yet staged would spill registers of the promotion loop.
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float b = epi_load(g.bias, g.bias_t, bias_at + 8 * c + k);
+                        const float d = epi_load(g.bias, g.bias_t, bias_at + g.n_out + 8 * c + k);
+#pragma unroll
+                        for (int i = 0; i < N; ++i) { z[i][k] += b; u[i][k] += d; }
+                    }
+                } else {
+                    float bz[8];
+                    epi_bias8(g, bias_at + 8 * c, bz);
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) z[i][k] += bz[k];
+                }
+            }
+            if (!GATED && g.pre) {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (r0 + i * RSTEP < rows) epi_store8(g.pre, g.c_t, (row0 + r0 + i * RSTEP) * g.n_out + j, z[i]);
+            }
+            epi_act(g.act, z);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if constexpr (GATED) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) z[i][k] *= u[i][k];
+                } else {
+                    if (g.residual) epi_add8(g.c_t, res[i], z[i]);
+                }
+                if (r0 + i * RSTEP < rows) epi_store8(g.c, g.c_t, (row0 + r0 + i * RSTEP) * g.n_out + j, z[i]);
+            }
+        }
+    } else if (!GATED && col + lane < g.n_out) {
+        // Odd widths, and the last columns: a lane per column.
+        const float b = g.bias ? epi_load(g.bias, g.bias_t, bias_at + lane) : 0.0f;
+        for (int r = 0; r < rows; ++r) {
+            const int64_t at = (row0 + r) * g.n_out + col + lane;
+            float z = stage[r * 4 * ROW4 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)] + b;
+            if (g.pre) epi_store(g.pre, g.c_t, at, z);
+            z = epi_act1(g.act, z);
+            if (g.residual) z += epi_load(g.residual, g.c_t, at);
+            epi_store(g.c, g.c_t, at, z);
         }
     }
-    __syncwarp();                                   // read before the next chunk is staged
+}
+
+// A tile's columns of one warp: acc holds two runs of SW columns of this lane's
+// row; plain: consecutive ones from column col; gated: from col of each half.
+// They are staged COLS at a time: consecutive ones, or half as many of each run. The sums still in registers beside the epilogue's code cost the
+// promotion loop spilled registers, so as many leave at once as the staging holds.
+template <int SW>
+struct EpiPlan {
+    static constexpr int COLS = SW == 64 ? 64 : 32;
+    static constexpr uint32_t WARP_BYTES = 32 * COLS * 4;
+};
+template <int SW, bool GATED>
+__device__ __forceinline__ void epi_tile(const EpiArgs& g, float* stage, int lane, int64_t row0, int rows, int64_t col,
+                                         int64_t bias_at, bool row_in, const F2 (&acc)[SW]) {
+    constexpr int COLS = EpiPlan<SW>::COLS, ROW4 = COLS / 4;      // staged columns
+#pragma unroll
+    for (int part = 0; part < 2 * SW / COLS; ++part) {
+        if constexpr (GATED) {
+            // 16 columns of the gate, the same 16 of the other half, and so on.
+#pragma unroll
+            for (int c = 0; c < COLS / 32; ++c) {
+                epi_stage<ROW4>(stage, lane, row_in, 8 * c, acc, part * COLS / 4 + 8 * c, 16);
+                epi_stage<ROW4>(stage, lane, row_in, 8 * c + 4, acc, SW / 2 + part * COLS / 4 + 8 * c, 16);
+            }
+        } else {
+            epi_stage<ROW4>(stage, lane, row_in, 0, acc, part * COLS / 2, COLS);
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < COLS / 32; ++c) {
+            const int64_t at = col + (GATED ? 16 : 32) * (part * (COLS / 32) + c);
+            if (at < g.n_out)                           // uniform over the warp
+                epi_chunk<GATED, GATED ? 1 : 4, ROW4>(g, stage + 32 * c, lane, row0, rows, at, bias_at + (at - col));
+        }
+        __syncwarp();                                   // read before the next part is staged
+    }
 }
 
 }  // namespace

@@ -206,6 +206,68 @@ __device__ __forceinline__ uint64_t desc_k_sw128(uint32_t saddr) {
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// The block scales of four k-blocks from kb on, of [.., kend); zeros past the end
+// and unless `use`. One 16-byte load where `vec` says that rows of scales start
+// on 16-byte boundaries. Promotion loops load a group ahead: next to a full
+// stream of operand tiles a load takes longer than two k-blocks.
+struct Scales4 {
+    float v[4];
+};
+__device__ __forceinline__ Scales4 load_scales4(const float* row, int kb, int kend, bool use, bool vec) {
+    Scales4 s;
+    if (use && vec && kb + 4 <= kend) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(row + kb));
+        s.v[0] = f.x; s.v[1] = f.y; s.v[2] = f.z; s.v[3] = f.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s.v[j] = use && kb + j < kend ? __ldg(row + kb + j) : 0.0f;
+    }
+    return s;
+}
+
+// Position in a ring of N slots: the slot, and the parity of its current round.
+template <int N>
+struct Ring {
+    int slot = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) { slot = 0; round ^= 1u; }
+    }
+};
+// 16 or 4 bytes from global to shared memory, asynchronously.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
+}
+// This thread's arrival on the barrier, when its copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Block scales through shared memory: a ring of groups of four k-blocks, each
+// with 16 bytes per row of the tile (128) and per set of weight scales (two).
+// A promotion loop whose registers are full of sums must not have loads from
+// global memory in flight: the loop that fetched its own scales ran at 980 to
+// 1650 clocks a k-block, depending on how the compiler placed the loads.
+constexpr int SG = 4;                                  // groups of the ring
+constexpr uint32_t SG_BYTES = (128 + 2) * 16;
+// Four scales from k-block kb of a row of them; those past kend are left out.
+__device__ __forceinline__ void copy_scales4(uint32_t dst, const float* row, int kb, int kend, bool vec) {
+    if (vec && kb + 4 <= kend) {
+        copy16(dst, row + kb);
+    } else {
+        for (int j = 0; j < 4 && kb + j < kend; ++j) copy4(dst + 4u * (uint32_t)j, row + kb + j);
+    }
+}
+__device__ __forceinline__ float ld_shared1(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 [[maybe_unused]] cudaError_t encode_map(CUtensorMap* tm, CUtensorMapDataType dt, const void* p, uint64_t inner,
                        uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer) {
     static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {

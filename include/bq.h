@@ -683,7 +683,7 @@ bq_status bq_moe_combine_backward(const void* dout, const void* y, bq_dtype dtyp
  *   c       [c_rows, n or n/2] F32, F16 or BF16, 16-byte aligned. Rows outside
  *           every expert's range are left as they were.
  * k % 128 == 0; gated: n % 256 == 0; n_experts <= 1024; a_rows, c_rows and
- * n_experts * n < 2^31. Accuracy as for the dense products. One launch. */
+ * n_experts * n < 2^31 - 256; with rows a_rows * k < 2^36. Accuracy as for the dense products. One launch. */
 bq_status bq_fp8_grouped_gemm(const uint8_t* a_e4m3, const float* a_scale, int64_t a_rows, int64_t k,
                               const int32_t* rows, const int32_t* offsets, int32_t n_experts,
                               int64_t c_rows, const uint8_t* w_e4m3, const float* w_scale, int64_t n,

@@ -119,9 +119,9 @@ def test_binding_checks_shapes_and_devices(B):
         bq.api.moe_group(torch.zeros((4, 2), dtype=torch.int32), 8)
     need = B._need
     t = torch.zeros((4, 6), device="meta")
-    for shape, dtype, like in (((4, 7), None, t), ((4,), None, t), ((4, 6), torch.float16, t), ((4, 6), None, x)):
+    for shape, dtypes in (((4, 7), (torch.float32,)), ((4,), (torch.float32,)), ((4, 6), (torch.float16,)), ((4, 6), (torch.float32,))):
         with pytest.raises(ValueError):
-            need(t, "t", shape, dtype, like)
-    with pytest.raises(ValueError):
-        need(t.t(), "t", (6, 4), None, t)
-    assert need(None, "t", (1,)) is None
+            need(t, "t", shape, dtypes, 0)
+    with pytest.raises(ValueError, match="contiguous"):
+        need(t.t(), "t", (6, 4), (torch.float32,), 0)
+    assert need(None, "t", (1,), (torch.float32,), 0) is None
