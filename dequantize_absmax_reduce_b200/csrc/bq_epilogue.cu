@@ -45,24 +45,39 @@ __global__ void __launch_bounds__(EB_COLS* EB_ROWS) k_epi_bwd(const EpiBwdArgs a
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
     if (col < a.n) {
-        for (int64_t r = r0 + ry; r < r1; r += EB_ROWS) {
-            const int64_t at = r * a.n + col;
+        // Four rows of a thread in flight.
+        for (int64_t r = r0 + ry; r < r1; r += 4 * EB_ROWS) {
+            U4 gv[4], zv[4];
             float g[V], z[V];
-            if constexpr (V > 1) {
-                load_vec<T>(ld16_nc(pre + at), z);
-                // dz may be dy itself: an ordinary load, before the store below.
-                load_vec<T>(*reinterpret_cast<const U4*>(dy + at), g);
-            } else {
-                z[0] = ld1<T>(pre + at);
-                g[0] = (float)dy[at];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t at = (r + q * EB_ROWS) * a.n + col;
+                if (r + q * EB_ROWS >= r1) break;
+                if constexpr (V > 1) {
+                    zv[q] = ld16_stream(pre + at);
+                    // dz may be dy itself: an ordinary load, before the stores below.
+                    gv[q] = *reinterpret_cast<const U4*>(dy + at);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                g[i] *= act_slope<ACT>(z[i]);
-                acc[i] += g[i];
+            for (int q = 0; q < 4; ++q) {
+                const int64_t at = (r + q * EB_ROWS) * a.n + col;
+                if (r + q * EB_ROWS >= r1) break;
+                if constexpr (V > 1) {
+                    load_vec<T>(zv[q], z);
+                    load_vec<T>(gv[q], g);
+                } else {
+                    z[0] = ld1<T>(pre + at);
+                    g[0] = (float)dy[at];
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    g[i] *= act_slope<ACT>(z[i]);
+                    acc[i] += g[i];
+                }
+                if constexpr (V > 1) st16(dz + at, pack_vec<T>(g));
+                else dz[at] = to_out<T>(g[0]);
             }
-            if constexpr (V > 1) st16(dz + at, pack_vec<T>(g));
-            else dz[at] = to_out<T>(g[0]);
         }
     }
     pdl_trigger();

@@ -5,6 +5,7 @@
 #include <math_constants.h>
 
 #include "bq.h"
+#include "bq_act.cuh"
 #include "bq_device.cuh"
 #include "bq_internal.h"
 
@@ -16,14 +17,26 @@ constexpr unsigned FULL = 0xffffffffu;
 // ---------------------------------------------------------------- routing
 // One warp per token. Lane l holds the C consecutive experts from l * C, so
 // that the lowest lane with the largest value holds the lowest index of it.
-// The order of the choice values decides which experts a token gets, so they
-// are computed in f64, where two different logits practically never give
-// equal values.
+//
+// The order of the choice values decides which experts a token gets, and it is
+// the order of f64 arithmetic. Without a bias the values are the logits, which
+// 32 bits hold exactly. With one, scores in f32 are off by less than 28 * 2^-24
+// (softmax: an exponential within 2 ulp, its argument's rounding, ten levels of a
+// sum of such terms, a reciprocal and a product, on values of at most 1; a sigmoid
+// has less) and the sum with the bias by 2^-24 of its size: where two values that
+// decide are nearer than 2^-18 max(1, |v|) (sums of two: 2^-17), the row is chosen
+// once more in f64 by route_exact. That happens to about one row in a hundred of 256
+// experts; in f64 throughout, 16384 such rows took 65 us.
+//
+// A lane keeps its two best values; a choice takes the largest over the warp
+// (one redux on the order-preserving integers) and its lane moves up its second.
+// Only a lane that is asked for a third looks through its values again.
 struct RouteArgs {
     const void* logits;
     const float* bias;
     int64_t tokens;
     int experts, top_k, n_groups, top_groups, group_top, sigmoid, renorm, vec;
+    int group_lanes;           // lanes of a group, a power of two, or 0: groups do not end with lanes
     float scale;
     int32_t* ids;
     float* weights;
@@ -55,102 +68,260 @@ __device__ __forceinline__ void load_logits(const T* row, int lane, int experts,
     for (int i = 0; i < C; ++i) x[i] = e0 + i < experts ? ld1<T>(row + e0 + i) : -CUDART_INF_F;
 }
 
+__device__ __forceinline__ float warp_sum(float v) {
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    return v;
+}
+// exp(a - b) for a <= b, without the rounding of the difference, which would cost
+// |a - b| half steps: the part lost to it (Knuth's exact sum) comes back to first
+// order. 1 where they are equal, infinities among them.
+__device__ __forceinline__ float exp_diff(float a, float b) {
+    const float d = a - b;
+    if (a == b) return 1.0f;
+    if (!(d > -150.0f)) return 0.0f;
+    const float part = d - a, lost = (a - (d - part)) - (b + part);
+    const float e = expf(d);
+    return fmaf(e, lost, e);
+}
+// Integers in the order of floats; above 0, which stands for "not available".
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t b = __float_as_uint(v);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// The choice of one row in f64, from its logits in memory: returns the id that
+// lane j < top_k holds. vs: room for the row's choice values.
+template <class T>
+__device__ __noinline__ int route_exact(const RouteArgs& a, const T* row, int lane, double* vs) {
+    double top = -CUDART_INF, sum = 0.0;
+    if (!a.sigmoid) {
+        for (int e = lane; e < a.experts; e += 32) {
+            const double x = (double)ld1<T>(row + e);
+            if (x > top) top = x;
+        }
+        top = warp_max(top);
+        for (int e = lane; e < a.experts; e += 32) {
+            const double x = (double)ld1<T>(row + e);
+            if (x == x) sum += exp(x == top ? 0.0 : x - top);
+        }
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+    }
+    for (int e = lane; e < a.experts; e += 32) {
+        const double x = (double)ld1<T>(row + e);
+        const double s = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x == top ? 0.0 : x - top) / sum;
+        double v = a.bias ? s + (double)__ldg(a.bias + e) : x;
+        if (!(x > -CUDART_INF) || v != v) v = -CUDART_INF;
+        vs[e] = v;
+    }
+    __syncwarp();
+    if (a.n_groups > 1) {
+        const int gsize = a.experts / a.n_groups;
+        double gv = -CUDART_INF;
+        if (lane < a.n_groups) {
+            double b1 = -CUDART_INF, b2 = -CUDART_INF;
+            for (int j = 0; j < gsize; ++j) {
+                const double u = vs[lane * gsize + j];
+                if (u > b1) { b2 = b1; b1 = u; } else if (u > b2) b2 = u;
+            }
+            gv = b1;
+            if (a.group_top == 2 && b2 > -CUDART_INF) gv += b2;
+        }
+        int ahead = 0;
+        for (int j = 0; j < a.n_groups; ++j) {
+            const double o = __shfl_sync(FULL, gv, j);
+            ahead += (o > gv || (o == gv && j < lane)) ? 1 : 0;
+        }
+        const unsigned kept = __ballot_sync(FULL, lane < a.n_groups && ahead < a.top_groups);
+        for (int e = lane; e < a.experts; e += 32)
+            if (!((kept >> (e / gsize)) & 1u)) vs[e] = -CUDART_INF;
+        __syncwarp();
+    }
+    int id = -1;
+    for (int it = 0; it < a.top_k; ++it) {
+        double best = -CUDART_INF;
+        int bi = 0x7fffffff;
+        for (int e = lane; e < a.experts; e += 32)
+            if (vs[e] > best) { best = vs[e]; bi = e; }
+        for (int o = 16; o > 0; o >>= 1) {
+            const double ob = __shfl_xor_sync(FULL, best, o);
+            const int oi = __shfl_xor_sync(FULL, bi, o);
+            if (ob > best || (ob == best && oi < bi)) { best = ob; bi = oi; }
+        }
+        if (!(best > -CUDART_INF)) break;
+        if (lane == 0) vs[bi] = -CUDART_INF;
+        __syncwarp();
+        if (lane == it) id = bi;
+    }
+    __syncwarp();
+    return id;
+}
+
 template <class T, int C>
 __global__ void __launch_bounds__(128) k_moe_route(const RouteArgs a) {
     extern __shared__ double route_smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    double* vs = route_smem + (size_t)warp * a.experts;
+    double* room = route_smem + (size_t)warp * a.experts;
     const int gsize = a.experts / a.n_groups;
+    const bool scored = a.bias != nullptr;             // choice values are score + bias
+    float bias[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) bias[i] = scored && lane * C + i < a.experts ? __ldg(a.bias + lane * C + i) : 0.0f;
     for (int64_t t = (int64_t)blockIdx.x * 4 + warp; t < a.tokens; t += (int64_t)gridDim.x * 4) {
+        const T* row = reinterpret_cast<const T*>(a.logits) + t * a.experts;
         float x[C];
-        load_logits<T, C>(reinterpret_cast<const T*>(a.logits) + t * a.experts, lane, a.experts, a.vec, x);
+        load_logits<T, C>(row, lane, a.experts, a.vec, x);
         bool bad = false;
-        double top = -CUDART_INF;
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
-            if (x[i] != x[i]) { bad = true; x[i] = -CUDART_INF_F; }
-            top = fmax(top, (double)x[i]);
-        }
+        for (int i = 0; i < C; ++i) bad |= x[i] != x[i];
         bad = __any_sync(FULL, bad);
-        double s[C], v[C];
-        if (a.sigmoid) {
+        // The softmax's largest logit and sum, where scores enter.
+        float top = -CUDART_INF_F, inv = 0.0f, p[C];
+        if (!a.sigmoid) {
 #pragma unroll
-            for (int i = 0; i < C; ++i) s[i] = 1.0 / (1.0 + exp(-(double)x[i]));
-        } else {
+            for (int i = 0; i < C; ++i) top = fmaxf(top, x[i]);       // (a NaN is left out)
             top = warp_max(top);
-            double sum = 0.0;
+        }
+        if (!a.sigmoid && (scored || !a.renorm)) {
+            float part[C];
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                // Equal to the largest, -inf and +inf among them: exp(0).
-                s[i] = lane * C + i < a.experts ? exp((double)x[i] == top ? 0.0 : (double)x[i] - top) : 0.0;
-                sum += s[i];
+                p[i] = lane * C + i < a.experts && x[i] == x[i] ? expf(x[i] == top ? 0.0f : x[i] - top) : 0.0f;
+                part[i] = p[i];
             }
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
 #pragma unroll
-            for (int i = 0; i < C; ++i) s[i] /= sum;
+            for (int w = C / 2; w > 0; w /= 2)
+#pragma unroll
+                for (int i = 0; i < w; ++i) part[i] += part[i + w];
+            inv = 1.0f / warp_sum(part[0]);
         }
+        uint32_t key[C];
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const int e = lane * C + i;
-            v[i] = a.bias && e < a.experts ? s[i] + (double)__ldg(a.bias + e) : (double)x[i];
-            if (!(x[i] > -CUDART_INF_F) || v[i] != v[i]) v[i] = -CUDART_INF;
+            float v = x[i];
+            if (scored) v = (a.sigmoid ? logistic(x[i]) : p[i] * inv) + bias[i];
+            // (adding 0 makes one zero of the two)
+            key[i] = x[i] > -CUDART_INF_F && v > -CUDART_INF_F ? order_key(v + 0.0f) : 0u;
         }
-        if (a.n_groups > 1) {
+        // The two best of this lane.
+        uint32_t k1 = 0u, k2 = 0u;
+        int i1 = 0, i2 = 0;
+        auto best_two = [&](uint32_t below, int from) {   // of those behind (key below, index from)
+            k1 = k2 = 0u;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const uint32_t k = key[i] < below || (key[i] == below && i > from) ? key[i] : 0u;
+                if (k > k1) { k2 = k1; i2 = i1; k1 = k; i1 = i; }
+                else if (k > k2) { k2 = k; i2 = i; }
+            }
+        };
+        bool unsure = false;
+        if (a.n_groups > 1 && a.group_lanes == 0) {
+            // Groups that do not end with lanes: through shared memory.
+            float* vs = reinterpret_cast<float*>(room);
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < C; ++i)
-                if (lane * C + i < a.experts) vs[lane * C + i] = v[i];
+                if (lane * C + i < a.experts) reinterpret_cast<uint32_t*>(vs)[lane * C + i] = key[i];
             __syncwarp();
-            double gv = -CUDART_INF;
-            if (lane < a.n_groups) {
-                double b1 = -CUDART_INF, b2 = -CUDART_INF;
+            uint32_t g1 = 0u, g2 = 0u;
+            if (lane < a.n_groups)
                 for (int j = 0; j < gsize; ++j) {
-                    const double u = vs[lane * gsize + j];
-                    if (u > b1) { b2 = b1; b1 = u; } else if (u > b2) b2 = u;
+                    const uint32_t k = reinterpret_cast<uint32_t*>(vs)[lane * gsize + j];
+                    g2 = max(g2, min(k, g1));
+                    g1 = max(g1, k);
                 }
-                gv = b1;
-                if (a.group_top == 2 && b2 > -CUDART_INF) gv += b2;
-            }
+            const double gv = g1 == 0u ? -CUDART_INF
+                                       : (double)key_value(g1) + (a.group_top == 2 && g2 ? (double)key_value(g2) : 0.0);
             int ahead = 0;
             for (int j = 0; j < a.n_groups; ++j) {
                 const double o = __shfl_sync(FULL, gv, j);
                 ahead += (o > gv || (o == gv && j < lane)) ? 1 : 0;
+                unsure |= scored && j != lane && lane < a.n_groups && fabs(o - gv) <= 0x1p-17 * fmax(1.0, fabs(gv));
             }
             const unsigned kept = __ballot_sync(FULL, lane < a.n_groups && ahead < a.top_groups);
 #pragma unroll
             for (int i = 0; i < C; ++i) {
                 const int e = lane * C + i;
-                if (e < a.experts && !((kept >> (e / gsize)) & 1u)) v[i] = -CUDART_INF;
+                if (e < a.experts && !((kept >> (e / gsize)) & 1u)) key[i] = 0u;
+            }
+            best_two(0xffffffffu, -1);
+        } else {
+            best_two(0xffffffffu, -1);
+            if (a.n_groups > 1) {
+                uint32_t g1 = k1, g2 = k2;
+                for (int o = 1; o < a.group_lanes; o <<= 1) {
+                    const uint32_t o1 = __shfl_xor_sync(FULL, g1, o), o2 = __shfl_xor_sync(FULL, g2, o);
+                    g2 = max(max(g2, o2), min(g1, o1));
+                    g1 = max(g1, o1);
+                }
+                const int mine = lane / a.group_lanes;
+                const double gv = g1 == 0u ? -CUDART_INF
+                                           : (double)key_value(g1) + (a.group_top == 2 && g2 ? (double)key_value(g2) : 0.0);
+                int ahead = 0;
+                for (int j = 0; j < a.n_groups; ++j) {
+                    const double o = __shfl_sync(FULL, gv, j * a.group_lanes);
+                    ahead += (o > gv || (o == gv && j < mine)) ? 1 : 0;
+                    unsure |= scored && j != mine && mine < a.n_groups && fabs(o - gv) <= 0x1p-17 * fmax(1.0, fabs(gv));
+                }
+                if (mine >= a.n_groups || ahead >= a.top_groups) {
+#pragma unroll
+                    for (int i = 0; i < C; ++i) key[i] = 0u;
+                    k1 = k2 = 0u;
+                }
             }
         }
-        int my_id = -1;
-        double my_s = 0.0;
-        for (int it = 0; it < a.top_k; ++it) {
-            double best = -CUDART_INF, bs = 0.0;
-            int bi = 0x7fffffff;
-#pragma unroll
-            for (int i = 0; i < C; ++i)
-                if (v[i] > best) { best = v[i]; bs = s[i]; bi = lane * C + i; }
-            for (int o = 16; o > 0; o >>= 1) {
-                const double ob = __shfl_xor_sync(FULL, best, o), os = __shfl_xor_sync(FULL, bs, o);
-                const int oi = __shfl_xor_sync(FULL, bi, o);
-                if (ob > best || (ob == best && oi < bi)) { best = ob; bs = os; bi = oi; }
+        int id = -1;
+        uint32_t mine = 0u, next = 0u;                 // this lane's choice; the one behind the last
+        bool second = true;                            // (k2, i2) is this lane's second
+        for (int it = 0; it <= a.top_k; ++it) {
+            const uint32_t m = __reduce_max_sync(FULL, k1);
+            if (m == 0u) break;
+            if (it == a.top_k) { next = m; break; }
+            const int w = __ffs(__ballot_sync(FULL, k1 == m)) - 1;
+            const int got = __shfl_sync(FULL, (lane * C + i1) | (second ? 0 : 0x40000000), w);
+            const int e = got & 0x3fffffff;
+            if (lane == it) { id = e; mine = m; }
+            if (got & 0x40000000) {
+                if (lane == w) { best_two(m, e - w * C); second = true; }
+            } else if (lane == w) {
+                k1 = k2; i1 = i2; second = false;
             }
-            if (!(best > -CUDART_INF)) break;
-#pragma unroll
-            for (int i = 0; i < C; ++i)
-                if (lane * C + i == bi) v[i] = -CUDART_INF;
-            if (lane == it) { my_id = bi; my_s = bs; }
         }
-        double w = my_s;
-        if (a.renorm) {
-            double sum = w;
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
-            w = sum > 0.0 ? w / sum : 0.0;
+        if (scored) {
+            uint32_t behind = __shfl_down_sync(FULL, mine, 1);
+            if (lane == a.top_k - 1) behind = next;
+            if (lane < a.top_k && mine && behind) {
+                const float v = key_value(mine);
+                // (written so that infinities count as near)
+                unsure |= !(v - key_value(behind) > 0x1p-18f * fmaxf(1.0f, fabsf(v)));
+            }
+            if (__any_sync(FULL, unsure)) id = route_exact<T>(a, row, lane, room);
+        }
+        // Weights in f32; renormalised ones relative to the largest chosen, so
+        // that small scores keep their ratios.
+        const bool there = id >= 0 && lane < a.top_k;
+        const float l = there ? ld1<T>(row + id) : -CUDART_INF_F;
+        float w;
+        if (a.sigmoid || a.renorm) {
+            const float low = a.sigmoid ? fminf(l, 0.0f) : l;
+            const float ref = a.renorm ? warp_max(low) : 0.0f;
+            w = there ? exp_diff(low, ref) : 0.0f;
+            if (a.sigmoid) w = w / (1.0f + expf(-fabsf(l)));         // sigmoid = exp(min(l, 0)) / (1 + exp(-|l|))
+            if (a.renorm) {
+                // Where f64 has no score left (exp(-746) is 0), there is nothing to share.
+                const bool none = a.sigmoid ? ref < -745.0f : ref - top < -745.0f;
+                const float sum = warp_sum(there ? w : 0.0f);
+                w = sum > 0.0f && !none ? w / sum : 0.0f;
+            }
+        } else {
+            w = there ? exp_diff(l, top) * inv : 0.0f;
         }
         if (lane < a.top_k) {
-            a.ids[t * a.top_k + lane] = my_id;
-            a.weights[t * a.top_k + lane] = bad ? CUDART_NAN_F : (float)(w * (double)a.scale);
+            a.ids[t * a.top_k + lane] = id;
+            a.weights[t * a.top_k + lane] = bad ? CUDART_NAN_F : there ? w * a.scale : 0.0f;
         }
     }
 }
@@ -172,11 +343,6 @@ struct RouteBwdArgs {
     float scale;
     void* dlogits;
 };
-
-__device__ __forceinline__ float warp_sum(float v) {
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
-    return v;
-}
 
 template <class T, int C>
 __global__ void __launch_bounds__(128) k_moe_route_bwd(const RouteBwdArgs a) {
@@ -217,7 +383,7 @@ __global__ void __launch_bounds__(128) k_moe_route_bwd(const RouteBwdArgs a) {
             float s = 0.0f, tail = 1.0f;
             if (a.renorm) {
                 const float top = warp_max(low);
-                s = id >= 0 ? expf(low == top ? 0.0f : low - top) : 0.0f;
+                s = id >= 0 ? exp_diff(low, top) : 0.0f;
             } else {
                 s = id >= 0 ? expf(low) : 0.0f;
             }
@@ -293,7 +459,9 @@ struct RouteLaunch {
     static cudaError_t go(RouteArgs a, cudaStream_t st) {
         constexpr int VEC = Traits<T>::VEC;
         a.vec = a.experts % VEC == 0 && ((uintptr_t)a.logits & 15u) == 0;
-        const size_t smem = a.n_groups > 1 ? 4 * sizeof(double) * (size_t)a.experts : 0;
+        const int gsize = a.experts / a.n_groups, lanes = gsize / C;
+        a.group_lanes = gsize % C == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+        const size_t smem = 4 * sizeof(double) * (size_t)a.experts;
         k_moe_route<T, C><<<warp_grid(a.tokens, 16), 128, smem, st>>>(a);
         return cudaGetLastError();
     }
@@ -314,14 +482,19 @@ struct RouteBwdLaunch {
 // consecutive run of its CTA's. Pass one counts per warp and expert; prefix
 // sums over the warps, over the CTAs (through distributed shared memory) and
 // over the experts give every (warp, expert) its first position; pass two
-// hands out the positions in the order of the pairs. No atomics: the order
-// is the same every time.
-constexpr int GROUP_CTAS = 8, GROUP_NT = 1024, GROUP_WARPS = GROUP_NT / 32;
+// hands out the positions in the order of the pairs: a lane's place among the
+// equal experts of its 32 comes from ballots over the bits of the expert's
+// number. The same result every time (only the counts use atomics).
+// Bound by latency: a run's ids are loaded GROUP_ROWS at a time, so that few
+// loads from memory follow one another, and kept where they are all.
+constexpr int GROUP_CTAS = 8, GROUP_NT = 1024, GROUP_WARPS = GROUP_NT / 32, GROUP_ROWS = 16;
 
 struct GroupArgs {
     const int32_t* ids;
-    int64_t pairs;
-    int top_k, first, n;
+    int pairs;                 // below 2^31
+    int per;                   // pairs of a warp, a multiple of 32
+    int first, n, bits;        // bits: of the largest expert number, n itself (other experts) included
+    FastDiv top_k;
     int32_t *offsets, *rows, *pos;
 };
 
@@ -330,44 +503,58 @@ __global__ void __launch_bounds__(GROUP_NT, 1) k_moe_group(const GroupArgs a) {
     extern __shared__ int32_t group_smem[];
     int32_t* table = group_smem;                        // [GROUP_WARPS][n]
     int32_t* mine = table + (size_t)GROUP_WARPS * a.n;  // [n] this CTA's counts
-    int32_t* base = mine + a.n;                         // [n] first position of this CTA's run
     __shared__ int32_t warp_tot[GROUP_WARPS];
     __shared__ int32_t total_all;
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), ctas = (int)cl.num_blocks();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // Pairs of a warp: a multiple of 32, consecutive over (CTA, warp).
-    const int64_t per = ((a.pairs + (int64_t)ctas * GROUP_NT - 1) / ((int64_t)ctas * GROUP_NT)) * 32;
-    const int64_t lo = min(a.pairs, ((int64_t)rank * GROUP_WARPS + warp) * per), hi = min(a.pairs, lo + per);
+    const int64_t first_pair = ((int64_t)rank * GROUP_WARPS + warp) * a.per;
+    const int lo = (int)min((int64_t)a.pairs, first_pair), hi = (int)min((int64_t)a.pairs, first_pair + a.per);
     int32_t* tw = table + (size_t)warp * a.n;
+    int e[GROUP_ROWS];                                  // experts of GROUP_ROWS rows of 32 pairs; n: none of these
+    auto load = [&](int at) {
+#pragma unroll
+        for (int r = 0; r < GROUP_ROWS; ++r) {
+            e[r] = 32 * r + lane < hi - at ? __ldg(a.ids + at + 32 * r + lane) : -1;
+        }
+#pragma unroll
+        for (int r = 0; r < GROUP_ROWS; ++r) {
+            const unsigned u = (unsigned)e[r] - (unsigned)a.first;
+            e[r] = e[r] >= a.first && u < (unsigned)a.n ? (int)u : a.n;
+        }
+    };
     for (int i = lane; i < a.n; i += 32) tw[i] = 0;
     __syncwarp();
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-        const int64_t i = i0 + lane;
-        int e = i < hi ? a.ids[i] : -1;
-        e = e >= a.first && e - a.first < a.n ? e - a.first : -1;
-        const unsigned same = __match_any_sync(FULL, e);
-        if (e >= 0 && lane == __ffs(same) - 1) tw[e] += __popc(same);
-        __syncwarp();
+    for (int at = lo; at < hi; at += 32 * GROUP_ROWS) {
+        load(at);
+#pragma unroll
+        for (int r = 0; r < GROUP_ROWS; ++r)
+            if (e[r] < a.n) atomicAdd(tw + e[r], 1);
+        if (hi - at <= 32 * GROUP_ROWS) break;          // (at stays below 2^31)
     }
     __syncthreads();
-    for (int e = tid; e < a.n; e += GROUP_NT) {
-        int run = 0;
+    for (int x = tid; x < a.n; x += GROUP_NT) {
+        int c[GROUP_WARPS], run = 0;
+#pragma unroll
+        for (int w = 0; w < GROUP_WARPS; ++w) c[w] = table[w * a.n + x];
+#pragma unroll
         for (int w = 0; w < GROUP_WARPS; ++w) {
-            const int c = table[(size_t)w * a.n + e];
-            table[(size_t)w * a.n + e] = run;
-            run += c;
+            table[w * a.n + x] = run;
+            run += c[w];
         }
-        mine[e] = run;
+        mine[x] = run;
     }
-    cl.sync();
+    if (ctas > 1) cl.sync(); else __syncthreads();
     // Totals of every expert over the cluster, and of the CTAs before this one.
     int total = 0, before = 0;
     if (tid < a.n) {
-        for (int r = 0; r < ctas; ++r) {
-            const int c = cl.map_shared_rank(mine, r)[tid];
-            before += r < rank ? c : 0;
-            total += c;
+        int c[GROUP_CTAS];
+#pragma unroll
+        for (int r = 0; r < GROUP_CTAS; ++r) c[r] = r < ctas ? cl.map_shared_rank(mine, r)[tid] : 0;
+#pragma unroll
+        for (int r = 0; r < GROUP_CTAS; ++r) {
+            before += r < rank ? c[r] : 0;
+            total += c[r];
         }
     }
     int incl = total;
@@ -389,48 +576,63 @@ __global__ void __launch_bounds__(GROUP_NT, 1) k_moe_group(const GroupArgs a) {
     __syncthreads();
     const int excl = incl - total + (warp ? warp_tot[warp - 1] : 0);
     if (tid < a.n) {
-        base[tid] = excl + before;
+        // The first position of this CTA's run goes into every warp's row.
+        const int base = excl + before;
+#pragma unroll 8
+        for (int w = 0; w < GROUP_WARPS; ++w) table[w * a.n + tid] += base;
         if (rank == 0) {
             a.offsets[tid] = excl;
             if (tid == a.n - 1) a.offsets[a.n] = excl + total;
         }
     }
-    cl.sync();                     // no CTA leaves while another reads its counts
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-        const int64_t i = i0 + lane;
-        int e = i < hi ? a.ids[i] : -1;
-        e = e >= a.first && e - a.first < a.n ? e - a.first : -1;
-        const unsigned same = __match_any_sync(FULL, e);
-        int p = -1;
-        if (e >= 0) {
-            p = base[e] + tw[e] + __popc(same & ((1u << lane) - 1u));
-            a.rows[p] = (int32_t)(i / a.top_k);
+    __syncthreads();
+    const bool kept = hi - lo <= 32 * GROUP_ROWS;       // pass one's ids are all of them
+    for (int at = lo; at < hi; at += 32 * GROUP_ROWS) {
+        if (!kept) load(at);
+#pragma unroll
+        for (int r = 0; r < GROUP_ROWS; ++r) {
+            if (32 * r >= hi - at) break;               // uniform over the warp
+            const int i = at + 32 * r + min(lane, hi - at - 32 * r - 1);
+            unsigned same = FULL;
+            for (int bit = 0; bit < a.bits; ++bit) {
+                const unsigned set = __ballot_sync(FULL, (e[r] >> bit) & 1);
+                same &= (e[r] >> bit) & 1 ? set : ~set;
+            }
+            const bool in = e[r] < a.n;
+            const int p = in ? tw[e[r]] + __popc(same & ((1u << lane) - 1u)) : -1;
+            __syncwarp();
+            if (in && lane == 31 - __clz(same)) tw[e[r]] = p + 1;        // the last of the equal ones
+            __syncwarp();
+            if (in) a.rows[p] = (int32_t)fdiv((uint32_t)i, a.top_k);
+            if (32 * r + lane < hi - at) a.pos[i] = p;
         }
-        __syncwarp();
-        if (e >= 0 && lane == __ffs(same) - 1) tw[e] += __popc(same);
-        __syncwarp();
-        if (i < hi) a.pos[i] = p;
+        if (hi - at <= 32 * GROUP_ROWS) break;
     }
     // Rows behind the last expert's.
     for (int64_t i = total_all + (int64_t)rank * GROUP_NT + tid; i < a.pairs; i += (int64_t)ctas * GROUP_NT)
         a.rows[i] = -1;
+    if (ctas > 1) cl.sync();       // no CTA leaves while another reads its counts
 }
 
-cudaError_t launch_group(const GroupArgs& a, cudaStream_t st) {
-    const size_t smem = ((size_t)GROUP_WARPS + 2) * a.n * sizeof(int32_t);
+cudaError_t launch_group(GroupArgs a, cudaStream_t st) {
+    const size_t smem = ((size_t)GROUP_WARPS + 1) * a.n * sizeof(int32_t);
     static int ready[64] = {0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorUnknown;
     if (dev < 0 || dev >= 64) return cudaErrorNotSupported;
     if (!__atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE)) {
         const cudaError_t e = cudaFuncSetAttribute(k_moe_group, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (GROUP_WARPS + 2) * 1024 * (int)sizeof(int32_t));
+                                                   (GROUP_WARPS + 1) * 1024 * (int)sizeof(int32_t));
         if (e != cudaSuccess) return e;
         __atomic_store_n(&ready[dev], 1, __ATOMIC_RELEASE);
     }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
+    // One CTA alone while its warps have four rows of pairs at most.
     const unsigned ctas = a.pairs > 4 * GROUP_NT ? GROUP_CTAS : 1;
+    a.per = (int)(((int64_t)a.pairs + (int64_t)ctas * GROUP_NT - 1) / ((int64_t)ctas * GROUP_NT)) * 32;
+    a.bits = 1;
+    while ((a.n >> a.bits) != 0) ++a.bits;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ctas;
     attr[0].val.clusterDim.y = 1;
@@ -456,32 +658,83 @@ struct CombineArgs {
     const void* residual;
     void* out;
     int64_t tokens, y_rows, hidden, per_row;   // per_row: vectors of a row
-    int top_k;
+    int top_k, narrow;                         // narrow: all vectors are counted in 32 bits
+    FastDiv div;                               // by per_row
 };
 
+// V columns of a row as f32, and rounded from f32.
+template <class T, int V>
+__device__ __forceinline__ void load_cols(const T* p, float (&v)[V]) {
+    if constexpr (V * sizeof(T) >= 16) {
+        constexpr int N = Traits<T>::VEC;
+#pragma unroll
+        for (int i = 0; i < V; i += N) {
+            float x[N];
+            load_vec<T>(*reinterpret_cast<const U4*>(p + i), x);
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[i + j] = x[j];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = (float)p[i];
+    }
+}
+template <class T, int V>
+__device__ __forceinline__ void store_cols(T* p, const float (&v)[V]) {
+    if constexpr (V * sizeof(T) >= 16) {
+        constexpr int N = Traits<T>::VEC;
+#pragma unroll
+        for (int i = 0; i < V; i += N) {
+            float x[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[j] = v[i + j];
+            st16(p + i, pack_vec<T>(x));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = to_out<T>(v[i]);
+    }
+}
+
+// The rows of four slots are in flight at a time.
 template <class TY, class TO, int V>
 __global__ void __launch_bounds__(256) k_moe_combine(const CombineArgs a) {
     const int64_t total = a.tokens * a.per_row;
     for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (int64_t)gridDim.x * 256) {
-        const int64_t t = u / a.per_row, c = (u - t * a.per_row) * V;
+        int64_t t;
+        if (a.narrow) t = fdiv((uint32_t)u, a.div); else t = u / a.per_row;
+        const int64_t c = (u - t * a.per_row) * V;
         const TY* y = reinterpret_cast<const TY*>(a.y) + c;
-        float acc[V];
         const TO* res = reinterpret_cast<const TO*>(a.residual);
+        float r[V];
+        if (res) load_cols<TO, V>(res + t * a.hidden + c, r);
+        float acc[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-        for (int j = 0; j < a.top_k; ++j) {
-            const int64_t p = __ldg(a.pos + t * a.top_k + j);
-            if (p < 0 || p >= a.y_rows) continue;
-            const float w = __ldg(a.weights + t * a.top_k + j);
+        for (int j0 = 0; j0 < a.top_k; j0 += 4) {
+            int p[4];
+            float w[4], v[4][V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = fmaf(w, ld1<TY>(y + p * a.hidden + i), acc[i]);
-        }
-        TO* o = reinterpret_cast<TO*>(a.out) + t * a.hidden + c;
+            for (int j = 0; j < 4; ++j) {
+                p[j] = j0 + j < a.top_k ? __ldg(a.pos + t * a.top_k + j0 + j) : -1;
+                w[j] = j0 + j < a.top_k ? __ldg(a.weights + t * a.top_k + j0 + j) : 0.0f;
+                if (p[j] >= a.y_rows) p[j] = -1;
+            }
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (res) acc[i] += (float)res[t * a.hidden + c + i];
-            o[i] = to_out<TO>(acc[i]);
+            for (int j = 0; j < 4; ++j)
+                if (p[j] >= 0) load_cols<TY, V>(y + p[j] * a.hidden, v[j]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (p[j] >= 0) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[i] = fmaf(w[j], v[j][i], acc[i]);
+                }
         }
+        if (res) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] += r[i];
+        }
+        store_cols<TO, V>(reinterpret_cast<TO*>(a.out) + t * a.hidden + c, acc);
     }
 }
 
@@ -496,27 +749,48 @@ struct CombineBwdArgs {
     int top_k;
 };
 
-template <class T>
+template <class T, int V>
 __global__ void __launch_bounds__(128) k_moe_combine_bwd(const CombineBwdArgs a) {
     __shared__ float part[32][4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
         const T* dout = reinterpret_cast<const T*>(a.dout) + t * a.hidden;
-        for (int j = 0; j < a.top_k; ++j) {
-            const int64_t p = a.pos[t * a.top_k + j];
-            float dot = 0.0f;
-            if (p >= 0 && p < a.y_rows) {
-                const float w = a.weights[t * a.top_k + j];
-                const T* y = reinterpret_cast<const T*>(a.y) + p * a.hidden;
-                T* dy = reinterpret_cast<T*>(a.dy) + p * a.hidden;
-                for (int64_t c = threadIdx.x; c < a.hidden; c += 128) {
-                    const float d = ld1<T>(dout + c);
-                    dot = fmaf(d, ld1<T>(y + c), dot);
-                    dy[c] = to_out<T>(w * d);
-                }
+        // Four slots at a time: their rows are in flight together; dout comes
+        // from the first level cache for all but the first four.
+        for (int j0 = 0; j0 < a.top_k; j0 += 4) {
+            int64_t p[4];
+            float w[4], dot[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                p[j] = j0 + j < a.top_k ? __ldg(a.pos + t * a.top_k + j0 + j) : -1;
+                w[j] = j0 + j < a.top_k ? __ldg(a.weights + t * a.top_k + j0 + j) : 0.0f;
+                if (p[j] >= a.y_rows) p[j] = -1;
+                dot[j] = 0.0f;
             }
-            dot = warp_sum(dot);
-            if (lane == 0) part[j][warp] = dot;
+#pragma unroll 2
+            for (int64_t c = (int64_t)threadIdx.x * V; c < a.hidden; c += 128 * V) {
+                float d[V], y[4][V];
+                load_cols<T, V>(dout + c, d);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (p[j] >= 0) load_cols<T, V>(reinterpret_cast<const T*>(a.y) + p[j] * a.hidden + c, y[j]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (p[j] >= 0) {
+                        float o[V];
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            dot[j] = fmaf(d[i], y[j][i], dot[j]);
+                            o[i] = w[j] * d[i];
+                        }
+                        store_cols<T, V>(reinterpret_cast<T*>(a.dy) + p[j] * a.hidden + c, o);
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float s = warp_sum(dot[j]);
+                if (lane == 0 && j0 + j < a.top_k) part[j0 + j][warp] = s;
+            }
         }
         __syncthreads();
         if (threadIdx.x < a.top_k) {
@@ -528,11 +802,18 @@ __global__ void __launch_bounds__(128) k_moe_combine_bwd(const CombineBwdArgs a)
     }
 }
 
+// Vectors of eight columns where a row's columns and the tensors' starts allow
+// 16-byte accesses.
 template <class TY, class TO>
 cudaError_t launch_combine(CombineArgs a, cudaStream_t st) {
-    a.per_row = a.hidden;
-    const int64_t need = (a.tokens * a.per_row + 255) / 256, most = (int64_t)sm_count() * 64;
-    k_moe_combine<TY, TO, 1><<<(unsigned)(need < most ? need : most), 256, 0, st>>>(a);
+    const bool vec = a.hidden % 8 == 0 && (((uintptr_t)a.y | (uintptr_t)a.residual | (uintptr_t)a.out) & 15u) == 0;
+    a.per_row = vec ? a.hidden / 8 : a.hidden;
+    const int64_t total = a.tokens * a.per_row, blocks = (total + 255) / 256, most = 1 << 20;
+    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+    a.narrow = total < (1ll << 32);
+    a.div = make_fastdiv((uint32_t)a.per_row);
+    if (vec) k_moe_combine<TY, TO, 8><<<grid, 256, 0, st>>>(a);
+    else k_moe_combine<TY, TO, 1><<<grid, 256, 0, st>>>(a);
     return cudaGetLastError();
 }
 template <class TY>
@@ -543,8 +824,11 @@ cudaError_t combine_out(const CombineArgs& a, bq_dtype out, cudaStream_t st) {
 }
 template <class T>
 cudaError_t launch_combine_bwd(const CombineBwdArgs& a, cudaStream_t st) {
+    const bool vec = a.hidden % 8 == 0 && (((uintptr_t)a.dout | (uintptr_t)a.y | (uintptr_t)a.dy) & 15u) == 0;
     const int64_t most = (int64_t)sm_count() * 16;
-    k_moe_combine_bwd<T><<<(unsigned)(a.tokens < most ? a.tokens : most), 128, 0, st>>>(a);
+    const unsigned grid = (unsigned)(a.tokens < most ? a.tokens : most);
+    if (vec) k_moe_combine_bwd<T, 8><<<grid, 128, 0, st>>>(a);
+    else k_moe_combine_bwd<T, 1><<<grid, 128, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -576,7 +860,7 @@ extern "C" bq_status bq_moe_route(const void* logits, bq_dtype dtype, int64_t to
     if (misaligned(logits, type_mask(dtype)) || misaligned(bias, 3) || misaligned(ids, 3) || misaligned(weights, 3))
         return BQ_ERR_MISALIGNED;
     RouteArgs a{logits, bias, tokens, experts, top_k, n_groups, top_groups, group_top, score == BQ_SCORE_SIGMOID,
-                renormalize != 0, 0, scale, ids, weights};
+                renormalize != 0, 0, 0, scale, ids, weights};
     cudaStream_t st = (cudaStream_t)stream;
     if (dtype == BQ_F32) return from(by_width<float, RouteLaunch>(a, st));
     if (dtype == BQ_F16) return from(by_width<__half, RouteLaunch>(a, st));
@@ -608,7 +892,7 @@ extern "C" bq_status bq_moe_group(const int32_t* ids, int64_t tokens, int32_t to
         return BQ_ERR_INVALID_ARG;
     if (!offsets || (tokens > 0 && (!ids || !rows || !pos))) return BQ_ERR_INVALID_ARG;
     if (misaligned(ids, 3) || misaligned(offsets, 3) || misaligned(rows, 3) || misaligned(pos, 3)) return BQ_ERR_MISALIGNED;
-    GroupArgs a{ids, tokens * top_k, top_k, first_expert, n_experts, offsets, rows, pos};
+    GroupArgs a{ids, (int)(tokens * top_k), 0, first_expert, n_experts, 0, make_fastdiv((uint32_t)top_k), offsets, rows, pos};
     return from(launch_group(a, (cudaStream_t)stream));
 }
 
