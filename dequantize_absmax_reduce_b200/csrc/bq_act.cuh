@@ -14,39 +14,54 @@
 
 namespace bq {
 
-__device__ __forceinline__ float logistic(float x) {
+constexpr float kLog2e = 1.4426950408889634f;
+// 1 / (1 + 2^t)
+__device__ __forceinline__ float logistic_of(float t) {
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));   // exp(-x) = 2^(-x log2 e)
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return r;
 }
+__device__ __forceinline__ float logistic(float x) { return logistic_of(x * -kLog2e); }
 
 constexpr float kGeluA = 0.7978845608028654f;        // sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
+// s(2a) of the tanh form: the argument is z times an even polynomial.
+__device__ __forceinline__ float gelu_gate(float z) {
+    return logistic_of(z * fmaf(z * z, -2.0f * kLog2e * kGeluA * kGeluB, -2.0f * kLog2e * kGeluA));
+}
+// z within [-lim, lim]; a NaN stays one. The slopes below are 0 or 1 to the last
+// bit beyond their limits, where 0 * infinity would stand in their formulas.
+__device__ __forceinline__ float clamp_nan(float z, float lim) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(lim));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(r), "f"(-lim));
+    return r;
+}
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
     if constexpr (ACT == BQ_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
     else if constexpr (ACT == BQ_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
-    else if constexpr (ACT == BQ_ACT_GELU_TANH) return z * logistic(2.0f * kGeluA * fmaf(kGeluB * z * z, z, z));
+    else if constexpr (ACT == BQ_ACT_GELU_TANH) return z * gelu_gate(z);
     else if constexpr (ACT == BQ_ACT_SILU) return z * logistic(z);
     else return z;
 }
 
+// With s the logistic function of the activation's argument, d/dz z s = s (1 +
+// z (1 - s) times the argument's own slope).
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == BQ_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
     else if constexpr (ACT == BQ_ACT_GELU)
         return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), 0.5f * (1.0f + erff(z * 0.7071067811865476f)));
     else if constexpr (ACT == BQ_ACT_GELU_TANH) {
-        const float s = logistic(2.0f * kGeluA * fmaf(kGeluB * z * z, z, z));
-        // d/dz z s(2a): s + z s (1 - s) 2a'; s (1 - s) is 0 where z is so large that z a' overflows.
-        const float t = s * (1.0f - s);
-        return t == 0.0f ? s : fmaf(2.0f * kGeluA * z * t, fmaf(3.0f * kGeluB * z, z, 1.0f), s);
+        const float c = clamp_nan(z, 16.0f), s = gelu_gate(c);
+        const float q = c * fmaf(c * c, 6.0f * kGeluA * kGeluB, 2.0f * kGeluA);
+        return fmaf(s, fmaf(-s, q, q), s);
     } else if constexpr (ACT == BQ_ACT_SILU) {
-        const float s = logistic(z);
-        const float t = s * (1.0f - s);
-        return t == 0.0f ? s : fmaf(z, t, s);
+        const float c = clamp_nan(z, 126.0f), s = logistic(c);
+        return fmaf(s, fmaf(-s, c, c), s);
     } else return 1.0f;
 }
 

@@ -657,11 +657,35 @@ struct CombineArgs {
     const float* weights;
     const void* residual;
     void* out;
-    int64_t tokens, y_rows, hidden, per_row;   // per_row: vectors of a row
-    int top_k, narrow;                         // narrow: all vectors are counted in 32 bits
-    FastDiv div;                               // by per_row
+    int64_t tokens, y_rows, hidden;
+    int top_k;
 };
 
+// V columns of a row, as they lie in memory until their values are needed.
+template <class T, int V>
+struct Cols {
+    static constexpr bool WIDE = V * sizeof(T) >= 16;
+    static constexpr int N = WIDE ? V * (int)sizeof(T) / 16 : V;
+    typename std::conditional<WIDE, U4, T>::type raw[N];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) raw[i] = reinterpret_cast<const typename std::conditional<WIDE, U4, T>::type*>(p)[i];
+    }
+    __device__ __forceinline__ void values(float (&v)[V]) const {
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float x[Traits<T>::VEC];
+                load_vec<T>(raw[i], x);
+#pragma unroll
+                for (int j = 0; j < Traits<T>::VEC; ++j) v[i * Traits<T>::VEC + j] = x[j];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = (float)raw[i];
+        }
+    }
+};
 // V columns of a row as f32, and rounded from f32.
 template <class T, int V>
 __device__ __forceinline__ void load_cols(const T* p, float (&v)[V]) {
@@ -696,45 +720,58 @@ __device__ __forceinline__ void store_cols(T* p, const float (&v)[V]) {
     }
 }
 
-// The rows of four slots are in flight at a time.
+// A CTA takes a token (blockIdx.y: a share of its columns) and walks its columns
+// with the slots' positions in registers, the rows of eight slots (f32: four) in
+// flight at a time: with a thread per vector of the output, the wait for its
+// positions before every load held 4096 x 8 x 7168 at 140 us.
 template <class TY, class TO, int V>
-__global__ void __launch_bounds__(256) k_moe_combine(const CombineArgs a) {
-    const int64_t total = a.tokens * a.per_row;
-    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (int64_t)gridDim.x * 256) {
-        int64_t t;
-        if (a.narrow) t = fdiv((uint32_t)u, a.div); else t = u / a.per_row;
-        const int64_t c = (u - t * a.per_row) * V;
-        const TY* y = reinterpret_cast<const TY*>(a.y) + c;
-        const TO* res = reinterpret_cast<const TO*>(a.residual);
-        float r[V];
-        if (res) load_cols<TO, V>(res + t * a.hidden + c, r);
-        float acc[V];
+__global__ void __launch_bounds__(128) k_moe_combine(const CombineArgs a) {
+    constexpr int B = sizeof(TY) == 2 ? 8 : 4;
+    const TO* res = reinterpret_cast<const TO*>(a.residual);
+    for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+        const int32_t* pos = a.pos + t * a.top_k;
+        const float* weights = a.weights + t * a.top_k;
+        int p[B];
+        float w[B];
+        auto slots = [&](int j0) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-        for (int j0 = 0; j0 < a.top_k; j0 += 4) {
-            int p[4];
-            float w[4], v[4][V];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                p[j] = j0 + j < a.top_k ? __ldg(a.pos + t * a.top_k + j0 + j) : -1;
-                w[j] = j0 + j < a.top_k ? __ldg(a.weights + t * a.top_k + j0 + j) : 0.0f;
+            for (int j = 0; j < B; ++j) {
+                p[j] = j0 + j < a.top_k ? __ldg(pos + j0 + j) : -1;
+                w[j] = j0 + j < a.top_k ? __ldg(weights + j0 + j) : 0.0f;
                 if (p[j] >= a.y_rows) p[j] = -1;
             }
+        };
+        slots(0);
+        for (int64_t c = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * V; c < a.hidden; c += (int64_t)gridDim.y * blockDim.x * V) {
+            const TY* y = reinterpret_cast<const TY*>(a.y) + c;
+            float acc[V];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (p[j] >= 0) load_cols<TY, V>(y + p[j] * a.hidden, v[j]);
+            for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+            Cols<TO, V> r;
+            if (res) r.load(res + t * a.hidden + c);
+            for (int j0 = 0; j0 < a.top_k; j0 += B) {
+                if (a.top_k > B) slots(j0);
+                Cols<TY, V> v[B];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (p[j] >= 0) {
+                for (int j = 0; j < B; ++j)
+                    if (p[j] >= 0) v[j].load(y + p[j] * a.hidden);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) acc[i] = fmaf(w[j], v[j][i], acc[i]);
-                }
+                for (int j = 0; j < B; ++j)
+                    if (p[j] >= 0) {
+                        float x[V];
+                        v[j].values(x);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) acc[i] = fmaf(w[j], x[i], acc[i]);
+                    }
+            }
+            if (res) {
+                float x[V];
+                r.values(x);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] += x[i];
+            }
+            store_cols<TO, V>(reinterpret_cast<TO*>(a.out) + t * a.hidden + c, acc);
         }
-        if (res) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] += r[i];
-        }
-        store_cols<TO, V>(reinterpret_cast<TO*>(a.out) + t * a.hidden + c, acc);
     }
 }
 
@@ -755,41 +792,44 @@ __global__ void __launch_bounds__(128) k_moe_combine_bwd(const CombineBwdArgs a)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
         const T* dout = reinterpret_cast<const T*>(a.dout) + t * a.hidden;
-        // Four slots at a time: their rows are in flight together; dout comes
-        // from the first level cache for all but the first four.
-        for (int j0 = 0; j0 < a.top_k; j0 += 4) {
-            int64_t p[4];
-            float w[4], dot[4];
+        // Eight slots (f32: four) at a time: their rows are in flight together;
+        // dout comes from the first level cache for all but the first of them.
+        constexpr int B = sizeof(T) == 2 ? 8 : 4;
+        for (int j0 = 0; j0 < a.top_k; j0 += B) {
+            int p[B];
+            float w[B], dot[B];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < B; ++j) {
                 p[j] = j0 + j < a.top_k ? __ldg(a.pos + t * a.top_k + j0 + j) : -1;
                 w[j] = j0 + j < a.top_k ? __ldg(a.weights + t * a.top_k + j0 + j) : 0.0f;
                 if (p[j] >= a.y_rows) p[j] = -1;
                 dot[j] = 0.0f;
             }
-#pragma unroll 2
             for (int64_t c = (int64_t)threadIdx.x * V; c < a.hidden; c += 128 * V) {
-                float d[V], y[4][V];
+                float d[V];
+                Cols<T, V> y[B];
+#pragma unroll
+                for (int j = 0; j < B; ++j)
+                    if (p[j] >= 0) y[j].load(reinterpret_cast<const T*>(a.y) + p[j] * a.hidden + c);
                 load_cols<T, V>(dout + c, d);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (p[j] >= 0) load_cols<T, V>(reinterpret_cast<const T*>(a.y) + p[j] * a.hidden + c, y[j]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < B; ++j)
                     if (p[j] >= 0) {
-                        float o[V];
+                        float x[V], o[V];
+                        y[j].values(x);
 #pragma unroll
                         for (int i = 0; i < V; ++i) {
-                            dot[j] = fmaf(d[i], y[j][i], dot[j]);
+                            dot[j] = fmaf(d[i], x[i], dot[j]);
                             o[i] = w[j] * d[i];
                         }
                         store_cols<T, V>(reinterpret_cast<T*>(a.dy) + p[j] * a.hidden + c, o);
                     }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < B; ++j) {
+                if (j0 + j >= a.top_k) break;
                 const float s = warp_sum(dot[j]);
-                if (lane == 0 && j0 + j < a.top_k) part[j0 + j][warp] = s;
+                if (lane == 0) part[j0 + j][warp] = s;
             }
         }
         __syncthreads();
@@ -803,17 +843,18 @@ __global__ void __launch_bounds__(128) k_moe_combine_bwd(const CombineBwdArgs a)
 }
 
 // Vectors of eight columns where a row's columns and the tensors' starts allow
-// 16-byte accesses.
+// 16-byte accesses. As many threads as a row has vectors, 128 at most; few tokens
+// get several CTAs each.
 template <class TY, class TO>
-cudaError_t launch_combine(CombineArgs a, cudaStream_t st) {
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t st) {
     const bool vec = a.hidden % 8 == 0 && (((uintptr_t)a.y | (uintptr_t)a.residual | (uintptr_t)a.out) & 15u) == 0;
-    a.per_row = vec ? a.hidden / 8 : a.hidden;
-    const int64_t total = a.tokens * a.per_row, blocks = (total + 255) / 256, most = 1 << 20;
-    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
-    a.narrow = total < (1ll << 32);
-    a.div = make_fastdiv((uint32_t)a.per_row);
-    if (vec) k_moe_combine<TY, TO, 8><<<grid, 256, 0, st>>>(a);
-    else k_moe_combine<TY, TO, 1><<<grid, 256, 0, st>>>(a);
+    const int64_t per_row = vec ? a.hidden / 8 : a.hidden, sms = sm_count();
+    const unsigned threads = per_row >= 128 ? 128u : (unsigned)((per_row + 31) / 32 * 32);
+    const int64_t shares = (per_row + threads - 1) / threads, want = (4 * sms + a.tokens - 1) / a.tokens;
+    const int64_t gx = a.tokens < 16 * sms ? a.tokens : 16 * sms, gy = want < shares ? want : shares;
+    const dim3 grid((unsigned)gx, (unsigned)(gy < 65535 ? gy : 65535));
+    if (vec) k_moe_combine<TY, TO, 8><<<grid, threads, 0, st>>>(a);
+    else k_moe_combine<TY, TO, 1><<<grid, threads, 0, st>>>(a);
     return cudaGetLastError();
 }
 template <class TY>
@@ -907,7 +948,7 @@ extern "C" bq_status bq_moe_combine(const void* y, bq_dtype y_dtype, int64_t y_r
     if (misaligned(y, type_mask(y_dtype)) || misaligned(out, type_mask(out_dtype)) ||
         misaligned(residual, type_mask(out_dtype)) || misaligned(pos, 3) || misaligned(weights, 3))
         return BQ_ERR_MISALIGNED;
-    CombineArgs a{y, pos, weights, residual, out, tokens, y_rows, hidden, 0, top_k};
+    CombineArgs a{y, pos, weights, residual, out, tokens, y_rows, hidden, top_k};
     cudaStream_t st = (cudaStream_t)stream;
     if (y_dtype == BQ_F32) return from(combine_out<float>(a, out_dtype, st));
     if (y_dtype == BQ_F16) return from(combine_out<__half>(a, out_dtype, st));
