@@ -28,9 +28,11 @@ constexpr unsigned FULL = 0xffffffffu;
 // once more in f64 by route_exact. That happens to about one row in a hundred of 256
 // experts; in f64 throughout, 16384 such rows took 65 us.
 //
-// A lane keeps its two best values; a choice takes the largest over the warp
-// (one redux on the order-preserving integers) and its lane moves up its second.
-// Only a lane that is asked for a third looks through its values again.
+// A lane sorts its values once, as integers in their order whose lowest bits give
+// way to the value's number in the lane (the nearness test allows for that; so do
+// logits of 16 bits, which leave them free, and f32 logits that agree in all but
+// those bits go to route_exact too). A choice is then one redux over the lanes'
+// largest, one ballot, and its lane moves up its list.
 struct RouteArgs {
     const void* logits;
     const float* bias;
@@ -159,16 +161,37 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, const T* row, int la
     return id;
 }
 
-template <class T, int C>
+// Sorts v[0 .. C) downwards (Batcher's odd-even merge sort).
+template <int C>
+__device__ __forceinline__ void sort_down(uint32_t (&v)[C]) {
+#pragma unroll
+    for (int p = 1; p < C; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < C; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < C && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t hi = max(v[i + j], v[i + j + k]), lo = min(v[i + j], v[i + j + k]);
+                        v[i + j] = hi;
+                        v[i + j + k] = lo;
+                    }
+}
+
+// SCORED: choice values are score + bias; else the logits.
+template <class T, int C, bool SCORED>
 __global__ void __launch_bounds__(128) k_moe_route(const RouteArgs a) {
     extern __shared__ double route_smem[];
+    constexpr uint32_t LOW = C - 1;                    // bits that hold a value's number in its lane
+    using G = typename std::conditional<SCORED, float, double>::type;   // sums of a group's values
+    const G NONE = SCORED ? (G)-CUDART_INF_F : (G)-CUDART_INF;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     double* room = route_smem + (size_t)warp * a.experts;
     const int gsize = a.experts / a.n_groups;
-    const bool scored = a.bias != nullptr;             // choice values are score + bias
     float bias[C];
 #pragma unroll
-    for (int i = 0; i < C; ++i) bias[i] = scored && lane * C + i < a.experts ? __ldg(a.bias + lane * C + i) : 0.0f;
+    for (int i = 0; i < C; ++i) bias[i] = SCORED && lane * C + i < a.experts ? __ldg(a.bias + lane * C + i) : 0.0f;
     for (int64_t t = (int64_t)blockIdx.x * 4 + warp; t < a.tokens; t += (int64_t)gridDim.x * 4) {
         const T* row = reinterpret_cast<const T*>(a.logits) + t * a.experts;
         float x[C];
@@ -183,120 +206,107 @@ __global__ void __launch_bounds__(128) k_moe_route(const RouteArgs a) {
 #pragma unroll
             for (int i = 0; i < C; ++i) top = fmaxf(top, x[i]);       // (a NaN is left out)
             top = warp_max(top);
-        }
-        if (!a.sigmoid && (scored || !a.renorm)) {
-            float part[C];
+            if (SCORED || !a.renorm) {
+                float part[C];
 #pragma unroll
-            for (int i = 0; i < C; ++i) {
-                p[i] = lane * C + i < a.experts && x[i] == x[i] ? expf(x[i] == top ? 0.0f : x[i] - top) : 0.0f;
-                part[i] = p[i];
+                for (int i = 0; i < C; ++i) {
+                    p[i] = lane * C + i < a.experts && x[i] == x[i] ? expf(x[i] == top ? 0.0f : x[i] - top) : 0.0f;
+                    part[i] = p[i];
+                }
+#pragma unroll
+                for (int w = C / 2; w > 0; w /= 2)
+#pragma unroll
+                    for (int i = 0; i < w; ++i) part[i] += part[i + w];
+                inv = 1.0f / warp_sum(part[0]);
             }
-#pragma unroll
-            for (int w = C / 2; w > 0; w /= 2)
-#pragma unroll
-                for (int i = 0; i < w; ++i) part[i] += part[i + w];
-            inv = 1.0f / warp_sum(part[0]);
         }
         uint32_t key[C];
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             float v = x[i];
-            if (scored) v = (a.sigmoid ? logistic(x[i]) : p[i] * inv) + bias[i];
+            if (SCORED) v = (a.sigmoid ? logistic(x[i]) : p[i] * inv) + bias[i];
             // (adding 0 makes one zero of the two)
             key[i] = x[i] > -CUDART_INF_F && v > -CUDART_INF_F ? order_key(v + 0.0f) : 0u;
         }
-        // The two best of this lane.
-        uint32_t k1 = 0u, k2 = 0u;
-        int i1 = 0, i2 = 0;
-        auto best_two = [&](uint32_t below, int from) {   // of those behind (key below, index from)
-            k1 = k2 = 0u;
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-                const uint32_t k = key[i] < below || (key[i] == below && i > from) ? key[i] : 0u;
-                if (k > k1) { k2 = k1; i2 = i1; k1 = k; i1 = i; }
-                else if (k > k2) { k2 = k; i2 = i; }
-            }
-        };
         bool unsure = false;
-        if (a.n_groups > 1 && a.group_lanes == 0) {
-            // Groups that do not end with lanes: through shared memory.
-            float* vs = reinterpret_cast<float*>(room);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < C; ++i)
-                if (lane * C + i < a.experts) reinterpret_cast<uint32_t*>(vs)[lane * C + i] = key[i];
-            __syncwarp();
+        if (a.n_groups > 1) {
+            // A group's two best: of the lanes that hold it, or where groups do not
+            // end with lanes through shared memory.
             uint32_t g1 = 0u, g2 = 0u;
-            if (lane < a.n_groups)
-                for (int j = 0; j < gsize; ++j) {
-                    const uint32_t k = reinterpret_cast<uint32_t*>(vs)[lane * gsize + j];
-                    g2 = max(g2, min(k, g1));
-                    g1 = max(g1, k);
-                }
-            const double gv = g1 == 0u ? -CUDART_INF
-                                       : (double)key_value(g1) + (a.group_top == 2 && g2 ? (double)key_value(g2) : 0.0);
-            int ahead = 0;
-            for (int j = 0; j < a.n_groups; ++j) {
-                const double o = __shfl_sync(FULL, gv, j);
-                ahead += (o > gv || (o == gv && j < lane)) ? 1 : 0;
-                unsure |= scored && j != lane && lane < a.n_groups && fabs(o - gv) <= 0x1p-17 * fmax(1.0, fabs(gv));
-            }
-            const unsigned kept = __ballot_sync(FULL, lane < a.n_groups && ahead < a.top_groups);
+            auto enter = [&](uint32_t k) {
+                g2 = max(g2, min(k, g1));
+                g1 = max(g1, k);
+            };
+            const bool by_lane = a.group_lanes > 0;
+            int mine = lane, every = 1;                // this lane's group; lanes from one group to the next
+            if (by_lane) {
 #pragma unroll
-            for (int i = 0; i < C; ++i) {
-                const int e = lane * C + i;
-                if (e < a.experts && !((kept >> (e / gsize)) & 1u)) key[i] = 0u;
-            }
-            best_two(0xffffffffu, -1);
-        } else {
-            best_two(0xffffffffu, -1);
-            if (a.n_groups > 1) {
-                uint32_t g1 = k1, g2 = k2;
+                for (int i = 0; i < C; ++i) enter(key[i]);
                 for (int o = 1; o < a.group_lanes; o <<= 1) {
                     const uint32_t o1 = __shfl_xor_sync(FULL, g1, o), o2 = __shfl_xor_sync(FULL, g2, o);
                     g2 = max(max(g2, o2), min(g1, o1));
                     g1 = max(g1, o1);
                 }
-                const int mine = lane / a.group_lanes;
-                const double gv = g1 == 0u ? -CUDART_INF
-                                           : (double)key_value(g1) + (a.group_top == 2 && g2 ? (double)key_value(g2) : 0.0);
-                int ahead = 0;
-                for (int j = 0; j < a.n_groups; ++j) {
-                    const double o = __shfl_sync(FULL, gv, j * a.group_lanes);
-                    ahead += (o > gv || (o == gv && j < mine)) ? 1 : 0;
-                    unsure |= scored && j != mine && mine < a.n_groups && fabs(o - gv) <= 0x1p-17 * fmax(1.0, fabs(gv));
-                }
-                if (mine >= a.n_groups || ahead >= a.top_groups) {
+                every = a.group_lanes;
+                mine = lane / every;
+            } else {
+                uint32_t* vs = reinterpret_cast<uint32_t*>(room);
+                __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < C; ++i) key[i] = 0u;
-                    k1 = k2 = 0u;
+                for (int i = 0; i < C; ++i)
+                    if (lane * C + i < a.experts) vs[lane * C + i] = key[i];
+                __syncwarp();
+                if (lane < a.n_groups)
+                    for (int j = 0; j < gsize; ++j) enter(vs[lane * gsize + j]);
+            }
+            const G gv = g1 == 0u ? NONE : (G)key_value(g1) + (a.group_top == 2 && g2 ? (G)key_value(g2) : (G)0);
+            const G near = SCORED ? (G)(0x1p-17f * fmaxf(1.0f, fabsf((float)gv))) : (G)0;
+            int ahead = 0;
+            for (int j = 0; j < a.n_groups; ++j) {
+                const G o = __shfl_sync(FULL, gv, j * every);
+                ahead += o > gv || (o == gv && j < mine) ? 1 : 0;
+                // (a difference of infinities counts as near; groups with nothing are none's neighbours)
+                if (SCORED) unsure |= j != mine && mine < a.n_groups && gv > NONE && o > NONE && !(o > gv + near) && !(o < gv - near);
+            }
+            const bool kept = mine < a.n_groups && ahead < a.top_groups;
+            if (by_lane) {
+#pragma unroll
+                for (int i = 0; i < C; ++i) key[i] = kept ? key[i] : 0u;
+            } else {
+                const unsigned all = __ballot_sync(FULL, kept);
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    const int e = lane * C + i;
+                    if (e < a.experts && !((all >> (e / gsize)) & 1u)) key[i] = 0u;
                 }
             }
         }
+#pragma unroll
+        for (int i = 0; i < C; ++i) key[i] = key[i] ? (key[i] & ~LOW) | (LOW - i) : 0u;
+        sort_down<C>(key);
         int id = -1;
         uint32_t mine = 0u, next = 0u;                 // this lane's choice; the one behind the last
-        bool second = true;                            // (k2, i2) is this lane's second
         for (int it = 0; it <= a.top_k; ++it) {
-            const uint32_t m = __reduce_max_sync(FULL, k1);
+            const uint32_t head = key[0] & ~LOW, m = __reduce_max_sync(FULL, head);
             if (m == 0u) break;
             if (it == a.top_k) { next = m; break; }
-            const int w = __ffs(__ballot_sync(FULL, k1 == m)) - 1;
-            const int got = __shfl_sync(FULL, (lane * C + i1) | (second ? 0 : 0x40000000), w);
-            const int e = got & 0x3fffffff;
+            const int w = __ffs(__ballot_sync(FULL, head == m)) - 1;
+            const int e = __shfl_sync(FULL, lane * C + (int)(LOW - (key[0] & LOW)), w);
             if (lane == it) { id = e; mine = m; }
-            if (got & 0x40000000) {
-                if (lane == w) { best_two(m, e - w * C); second = true; }
-            } else if (lane == w) {
-                k1 = k2; i1 = i2; second = false;
+            if (lane == w) {
+#pragma unroll
+                for (int i = 0; i + 1 < C; ++i) key[i] = key[i + 1];
+                key[C - 1] = 0u;
             }
         }
-        if (scored) {
+        if (SCORED || std::is_same<T, float>::value) {
             uint32_t behind = __shfl_down_sync(FULL, mine, 1);
             if (lane == a.top_k - 1) behind = next;
             if (lane < a.top_k && mine && behind) {
                 const float v = key_value(mine);
                 // (written so that infinities count as near)
-                unsure |= !(v - key_value(behind) > 0x1p-18f * fmaxf(1.0f, fabsf(v)));
+                if (SCORED) unsure |= !(v - key_value(behind) > (0x1p-18f + C * 0x1p-22f) * fmaxf(1.0f, fabsf(v)));
+                else unsure |= mine == behind && C > 1;
             }
             if (__any_sync(FULL, unsure)) id = route_exact<T>(a, row, lane, room);
         }
@@ -462,7 +472,8 @@ struct RouteLaunch {
         const int gsize = a.experts / a.n_groups, lanes = gsize / C;
         a.group_lanes = gsize % C == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
         const size_t smem = 4 * sizeof(double) * (size_t)a.experts;
-        k_moe_route<T, C><<<warp_grid(a.tokens, 16), 128, smem, st>>>(a);
+        if (a.bias) k_moe_route<T, C, true><<<warp_grid(a.tokens, 16), 128, smem, st>>>(a);
+        else k_moe_route<T, C, false><<<warp_grid(a.tokens, 16), 128, smem, st>>>(a);
         return cudaGetLastError();
     }
 };
