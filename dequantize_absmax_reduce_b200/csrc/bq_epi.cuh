@@ -260,7 +260,7 @@ __device__ __forceinline__ void epi_tile(const EpiArgs& g, float* stage, int lan
         for (int c = 0; c < COLS / 32; ++c) {
             const int64_t at = col + (GATED ? 16 : 32) * (part * (COLS / 32) + c);
             if (at < g.n_out)                           // uniform over the warp
-                epi_chunk<GATED, GATED ? 1 : 4, ROW4>(g, stage + 32 * c, lane, row0, rows, at, bias_at + (at - col));
+                epi_chunk<GATED, GATED ? 1 : SW < 64 ? 2 : 4, ROW4>(g, stage + 32 * c, lane, row0, rows, at, bias_at + (at - col));
         }
         __syncwarp();                                   // read before the next part is staged
     }

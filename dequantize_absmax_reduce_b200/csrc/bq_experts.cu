@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(X_NT, 1) k_fp8_experts(const __grid_constant__
                 cluster_sync();
                 const uint32_t at = base + (uint32_t)(threadIdx.x - 128) * 16u;
                 constexpr uint32_t STEP = 256 * 16, PART = STEP * (SW / 2);
-                if (rank > 0) {
+                if (rank > 0 && lane < mine_rows) {              // rows that exist
                     const uint32_t dst = map_rank(at, 0u) + (uint32_t)(rank - 1) * PART;
 #pragma unroll
                     for (int j = 0; j < SW / 2; ++j) st_cluster_pair(dst + (uint32_t)j * STEP, acc[2 * j], acc[2 * j + 1]);
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(X_NT, 1) k_fp8_experts(const __grid_constant__
                 cluster_sync();
                 joined = true;
                 if (rank > 0) break;
-                for (int r = 0; r < parts - 1; ++r) {
+                for (int r = 0; r < parts - 1 && lane < mine_rows; ++r) {
 #pragma unroll
                     for (int j = 0; j < SW / 2; ++j) {
                         F2 x, y;

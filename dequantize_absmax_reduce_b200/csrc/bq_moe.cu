@@ -23,15 +23,17 @@ constexpr unsigned FULL = 0xffffffffu;
 // 32 bits hold exactly. With one, scores in f32 are off by less than 28 * 2^-24
 // (softmax: an exponential within 2 ulp, its argument's rounding, ten levels of a
 // sum of such terms, a reciprocal and a product, on values of at most 1; a sigmoid
-// has less) and the sum with the bias by 2^-24 of its size: where two values that
-// decide are nearer than 2^-18 max(1, |v|) (sums of two: 2^-17), the row is chosen
-// once more in f64 by route_exact. That happens to about one row in a hundred of 256
-// experts; in f64 throughout, 16384 such rows took 65 us.
+// has less) and the sum with the bias by 2^-24 of its size. Values nearer than
+// 2^-18 max(1, |v|) to one another, and what the keys' low bits take (sums of two:
+// 1.5 * 2^-17), are looked at again in f64: the candidates alone, those too near
+// the last to be told from it among them, or the groups' sums. That happens to
+// about one row in a hundred of 256 experts. In f64 throughout, 16384 such rows
+// took 65 us; with the near rows chosen anew in f64, their wait alone cost 7 us.
 //
 // A lane sorts its values once, as integers in their order whose lowest bits give
 // way to the value's number in the lane (the nearness test allows for that; so do
 // logits of 16 bits, which leave them free, and f32 logits that agree in all but
-// those bits go to route_exact too). A choice is then one redux over the lanes'
+// those bits are looked at again too). A choice is then one redux over the lanes'
 // largest, one ballot, and its lane moves up its list.
 struct RouteArgs {
     const void* logits;
@@ -39,6 +41,7 @@ struct RouteArgs {
     int64_t tokens;
     int experts, top_k, n_groups, top_groups, group_top, sigmoid, renorm, vec;
     int group_lanes;           // lanes of a group, a power of two, or 0: groups do not end with lanes
+    int sum_lanes;             // half the power of two that holds top_k
     float scale;
     int32_t* ids;
     float* weights;
@@ -94,70 +97,137 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// The choice of one row in f64, from its logits in memory: returns the id that
-// lane j < top_k holds. vs: room for the row's choice values.
-template <class T>
-__device__ __noinline__ int route_exact(const RouteArgs& a, const T* row, int lane, double* vs) {
-    double top = -CUDART_INF, sum = 0.0;
-    if (!a.sigmoid) {
-        for (int e = lane; e < a.experts; e += 32) {
-            const double x = (double)ld1<T>(row + e);
-            if (x > top) top = x;
-        }
+// A row's choice values in f64: the lane's C, from the logits in memory.
+template <class T, int C>
+__device__ __forceinline__ void exact_values(const RouteArgs& a, const T* row, int lane, double (&v)[C]) {
+    double x[C], top = -CUDART_INF, sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int e = lane * C + i;
+        x[i] = e < a.experts ? (double)ld1<T>(row + e) : -CUDART_INF;
+        if (x[i] > top) top = x[i];
+    }
+    if (a.bias && !a.sigmoid) {
         top = warp_max(top);
-        for (int e = lane; e < a.experts; e += 32) {
-            const double x = (double)ld1<T>(row + e);
-            if (x == x) sum += exp(x == top ? 0.0 : x - top);
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            v[i] = lane * C + i < a.experts && x[i] == x[i] ? exp(x[i] == top ? 0.0 : x[i] - top) : 0.0;
+            sum += v[i];
         }
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
     }
-    for (int e = lane; e < a.experts; e += 32) {
-        const double x = (double)ld1<T>(row + e);
-        const double s = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x == top ? 0.0 : x - top) / sum;
-        double v = a.bias ? s + (double)__ldg(a.bias + e) : x;
-        if (!(x > -CUDART_INF) || v != v) v = -CUDART_INF;
-        vs[e] = v;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int e = lane * C + i;
+        const double s = !a.bias ? x[i] : a.sigmoid ? 1.0 / (1.0 + exp(-x[i])) : v[i] / sum;
+        v[i] = a.bias && e < a.experts ? s + (double)__ldg(a.bias + e) : s;
+        if (!(x[i] > -CUDART_INF) || v[i] != v[i]) v[i] = -CUDART_INF;
     }
-    __syncwarp();
-    if (a.n_groups > 1) {
+}
+// The groups that stay, in f64: bit j of the result for the lane j that stands for
+// them (every lane of a group where groups end with lanes, else lane g for group
+// g). vs: room for the row's values.
+template <class T, int C>
+__device__ __noinline__ unsigned exact_groups(const RouteArgs& a, const T* row, int lane, double* vs) {
+    double v[C];
+    exact_values<T, C>(a, row, lane, v);
+    double b1 = -CUDART_INF, b2 = -CUDART_INF;
+    auto enter = [&](double u) {
+        if (u > b1) { b2 = b1; b1 = u; } else if (u > b2) b2 = u;
+    };
+    const bool by_lane = a.group_lanes > 0;
+    const int every = by_lane ? a.group_lanes : 1, mine = lane / every;
+    if (by_lane) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) enter(v[i]);
+        for (int o = 1; o < every; o <<= 1) {
+            const double o1 = __shfl_xor_sync(FULL, b1, o), o2 = __shfl_xor_sync(FULL, b2, o);
+            enter(o1);
+            enter(o2);
+        }
+    } else {
         const int gsize = a.experts / a.n_groups;
-        double gv = -CUDART_INF;
-        if (lane < a.n_groups) {
-            double b1 = -CUDART_INF, b2 = -CUDART_INF;
-            for (int j = 0; j < gsize; ++j) {
-                const double u = vs[lane * gsize + j];
-                if (u > b1) { b2 = b1; b1 = u; } else if (u > b2) b2 = u;
-            }
-            gv = b1;
-            if (a.group_top == 2 && b2 > -CUDART_INF) gv += b2;
-        }
-        int ahead = 0;
-        for (int j = 0; j < a.n_groups; ++j) {
-            const double o = __shfl_sync(FULL, gv, j);
-            ahead += (o > gv || (o == gv && j < lane)) ? 1 : 0;
-        }
-        const unsigned kept = __ballot_sync(FULL, lane < a.n_groups && ahead < a.top_groups);
-        for (int e = lane; e < a.experts; e += 32)
-            if (!((kept >> (e / gsize)) & 1u)) vs[e] = -CUDART_INF;
         __syncwarp();
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (lane * C + i < a.experts) vs[lane * C + i] = v[i];
+        __syncwarp();
+        if (lane < a.n_groups)
+            for (int j = 0; j < gsize; ++j) enter(vs[lane * gsize + j]);
+        __syncwarp();
+    }
+    double gv = b1;
+    if (a.group_top == 2 && b2 > -CUDART_INF) gv += b2;
+    int ahead = 0;
+    for (int j = 0; j < a.n_groups; ++j) {
+        const double o = __shfl_sync(FULL, gv, j * every);
+        ahead += (o > gv || (o == gv && j < mine)) ? 1 : 0;
+    }
+    return __ballot_sync(FULL, mine < a.n_groups && ahead < a.top_groups);
+}
+// The choice among the warp's candidates (lane j < n holds one, -1 elsewhere), by
+// their values in f64: returns the id of rank `lane` below top_k.
+template <class T, int C>
+__device__ __noinline__ int exact_order(const RouteArgs& a, const T* row, int lane, int id, int n, double* room) {
+    double v = -CUDART_INF;
+    if (a.bias && !a.sigmoid) {
+        double all[C];
+        exact_values<T, C>(a, row, lane, all);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (lane * C + i < a.experts) room[lane * C + i] = all[i];
+        __syncwarp();
+        if (id >= 0) v = room[id];
+        __syncwarp();
+    } else if (id >= 0) {
+        const double x = (double)ld1<T>(row + id);
+        v = a.bias ? 1.0 / (1.0 + exp(-x)) + (double)__ldg(a.bias + id) : x;
+    }
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+        const double o = __shfl_sync(FULL, v, j);
+        const int oi = __shfl_sync(FULL, id, j);
+        rank += o > v || (o == v && oi < id) ? 1 : 0;
+    }
+    int* to = reinterpret_cast<int*>(room);
+    if (id >= 0) to[rank] = id;
+    __syncwarp();
+    const int got = lane < n && lane < a.top_k ? to[lane] : -1;
+    __syncwarp();
+    return got;
+}
+// The choice of one row in f64 throughout, where more than 32 values are too near
+// one another: returns the id that lane j < top_k holds.
+template <class T, int C>
+__device__ __noinline__ int route_exact(const RouteArgs& a, const T* row, int lane, unsigned kept) {
+    double v[C];
+    exact_values<T, C>(a, row, lane, v);
+    const int gsize = a.experts / a.n_groups;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int e = lane * C + i;
+        const int bit = a.group_lanes > 0 ? lane : e / gsize;
+        if (a.n_groups > 1 && e < a.experts && !((kept >> bit) & 1u)) v[i] = -CUDART_INF;
     }
     int id = -1;
     for (int it = 0; it < a.top_k; ++it) {
         double best = -CUDART_INF;
         int bi = 0x7fffffff;
-        for (int e = lane; e < a.experts; e += 32)
-            if (vs[e] > best) { best = vs[e]; bi = e; }
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (v[i] > best) { best = v[i]; bi = lane * C + i; }
         for (int o = 16; o > 0; o >>= 1) {
             const double ob = __shfl_xor_sync(FULL, best, o);
             const int oi = __shfl_xor_sync(FULL, bi, o);
             if (ob > best || (ob == best && oi < bi)) { best = ob; bi = oi; }
         }
         if (!(best > -CUDART_INF)) break;
-        if (lane == 0) vs[bi] = -CUDART_INF;
-        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (lane * C + i == bi) v[i] = -CUDART_INF;
         if (lane == it) id = bi;
     }
-    __syncwarp();
     return id;
 }
 
@@ -179,33 +249,47 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[C]) {
                     }
 }
 
-// SCORED: choice values are score + bias; else the logits.
+// Whether two values (as masked keys, the larger first) may stand in another order in f64.
 template <class T, int C, bool SCORED>
-__global__ void __launch_bounds__(128) k_moe_route(const RouteArgs a) {
+__device__ __forceinline__ bool too_near(uint32_t hi, uint32_t lo) {
+    if constexpr (SCORED) {
+        const float v = key_value(hi);
+        // (written so that infinities count as near)
+        return !(v - key_value(lo) > (0x1p-18f + C * 0x1p-22f) * fmaxf(1.0f, fabsf(v)));
+    } else {
+        return std::is_same<T, float>::value && C > 1 && hi == lo;
+    }
+}
+
+// SCORED: choice values are score + bias; else the logits.
+// (Up to eight experts a lane seven CTAs share an SM: 26.0 us at 16384 x 256 in
+// groups with a bias, five 28.4, nine 27.7.)
+template <class T, int C, bool SCORED>
+__global__ void __launch_bounds__(128, C <= 8 ? 7 : 2) k_moe_route(const RouteArgs a) {
     extern __shared__ double route_smem[];
     constexpr uint32_t LOW = C - 1;                    // bits that hold a value's number in its lane
-    using G = typename std::conditional<SCORED, float, double>::type;   // sums of a group's values
-    const G NONE = SCORED ? (G)-CUDART_INF_F : (G)-CUDART_INF;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     double* room = route_smem + (size_t)warp * a.experts;
     const int gsize = a.experts / a.n_groups;
+    // Biases, and bits of the experts that are in service (a bias of -inf or NaN: never chosen).
     float bias[C];
+    uint32_t serve = 0u;
 #pragma unroll
-    for (int i = 0; i < C; ++i) bias[i] = SCORED && lane * C + i < a.experts ? __ldg(a.bias + lane * C + i) : 0.0f;
+    for (int i = 0; i < C; ++i) {
+        const bool in = lane * C + i < a.experts;
+        bias[i] = SCORED && in ? __ldg(a.bias + lane * C + i) : 0.0f;
+        serve |= in && bias[i] > -CUDART_INF_F ? 1u << i : 0u;
+    }
     for (int64_t t = (int64_t)blockIdx.x * 4 + warp; t < a.tokens; t += (int64_t)gridDim.x * 4) {
         const T* row = reinterpret_cast<const T*>(a.logits) + t * a.experts;
         float x[C];
         load_logits<T, C>(row, lane, a.experts, a.vec, x);
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < C; ++i) bad |= x[i] != x[i];
-        bad = __any_sync(FULL, bad);
         // The softmax's largest logit and sum, where scores enter.
         float top = -CUDART_INF_F, inv = 0.0f, p[C];
         if (!a.sigmoid) {
 #pragma unroll
             for (int i = 0; i < C; ++i) top = fmaxf(top, x[i]);       // (a NaN is left out)
-            top = warp_max(top);
+            top = key_value(__reduce_max_sync(FULL, order_key(top)));
             if (SCORED || !a.renorm) {
                 float part[C];
 #pragma unroll
@@ -220,15 +304,28 @@ __global__ void __launch_bounds__(128) k_moe_route(const RouteArgs a) {
                 inv = 1.0f / warp_sum(part[0]);
             }
         }
-        uint32_t key[C];
+        // Keys; 0: not available. Those of scores are packed at once, so that a
+        // group's sum is off by their low bits too; logits are packed below.
+        uint32_t key[C], least = 0xffffffffu;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            float v = x[i];
-            if (SCORED) v = (a.sigmoid ? logistic(x[i]) : p[i] * inv) + bias[i];
-            // (adding 0 makes one zero of the two)
-            key[i] = x[i] > -CUDART_INF_F && v > -CUDART_INF_F ? order_key(v + 0.0f) : 0u;
+            if (SCORED) {
+                const float v = (a.sigmoid ? logistic(x[i]) : p[i] * inv) + bias[i];
+                const uint32_t k = (order_key(v) & ~LOW) | (LOW - i);
+                key[i] = x[i] > -CUDART_INF_F && (serve & (1u << i)) ? k : 0u;
+            } else {
+                // (adding 0 makes one zero of the two)
+                key[i] = x[i] > -CUDART_INF_F && (serve & (1u << i)) ? order_key(x[i] + 0.0f) : 0u;
+            }
+            least = min(least, key[i]);
         }
-        bool unsure = false;
+        bool bad = false;                              // a NaN in the row
+        if (__any_sync(FULL, least == 0u)) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) bad |= x[i] != x[i];
+            bad = __any_sync(FULL, bad);
+        }
+        unsigned groups = FULL;                        // lanes, or groups, that stay
         if (a.n_groups > 1) {
             // A group's two best: of the lanes that hold it, or where groups do not
             // end with lanes through shared memory.
@@ -238,7 +335,7 @@ __global__ void __launch_bounds__(128) k_moe_route(const RouteArgs a) {
                 g1 = max(g1, k);
             };
             const bool by_lane = a.group_lanes > 0;
-            int mine = lane, every = 1;                // this lane's group; lanes from one group to the next
+            int mine = lane;                           // this lane's group
             if (by_lane) {
 #pragma unroll
                 for (int i = 0; i < C; ++i) enter(key[i]);
@@ -247,8 +344,7 @@ __global__ void __launch_bounds__(128) k_moe_route(const RouteArgs a) {
                     g2 = max(max(g2, o2), min(g1, o1));
                     g1 = max(g1, o1);
                 }
-                every = a.group_lanes;
-                mine = lane / every;
+                mine = lane >> (__ffs(a.group_lanes) - 1);
             } else {
                 uint32_t* vs = reinterpret_cast<uint32_t*>(room);
                 __syncwarp();
@@ -259,40 +355,67 @@ __global__ void __launch_bounds__(128) k_moe_route(const RouteArgs a) {
                 if (lane < a.n_groups)
                     for (int j = 0; j < gsize; ++j) enter(vs[lane * gsize + j]);
             }
-            const G gv = g1 == 0u ? NONE : (G)key_value(g1) + (a.group_top == 2 && g2 ? (G)key_value(g2) : (G)0);
-            const G near = SCORED ? (G)(0x1p-17f * fmaxf(1.0f, fabsf((float)gv))) : (G)0;
-            int ahead = 0;
-            for (int j = 0; j < a.n_groups; ++j) {
-                const G o = __shfl_sync(FULL, gv, j * every);
-                ahead += o > gv || (o == gv && j < mine) ? 1 : 0;
-                // (a difference of infinities counts as near; groups with nothing are none's neighbours)
-                if (SCORED) unsure |= j != mine && mine < a.n_groups && gv > NONE && o > NONE && !(o > gv + near) && !(o < gv - near);
+            bool kept = false, near = false;
+            if (SCORED || a.group_top == 1) {
+                // Values fit f32 (sums of scores: nearly): the best top_groups one by
+                // one, and whether the next one is near the last.
+                float gv = g1 ? key_value(g1) : -CUDART_INF_F;
+                if (a.group_top == 2 && g2) gv += key_value(g2);
+                uint32_t gk = g1 ? order_key(gv + 0.0f) : 0u, last = 0u;
+                for (int r = 0; r < a.top_groups; ++r) {
+                    const uint32_t m = __reduce_max_sync(FULL, gk);
+                    if (m == 0u) break;
+                    last = m;
+                    const int w = __shfl_sync(FULL, mine, __ffs(__ballot_sync(FULL, gk == m)) - 1);
+                    if (mine == w) { kept = true; gk = 0u; }
+                }
+                if (SCORED) {
+                    const uint32_t m = __reduce_max_sync(FULL, gk);
+                    const float v = key_value(last);
+                    // (written so that infinities count as near)
+                    near = m != 0u && !(v - key_value(m) > 0x1.8p-17f * fmaxf(1.0f, fabsf(v)) + C * 0x1p-22f * fabsf(v));
+                }
+            } else {
+                const int every = by_lane ? a.group_lanes : 1;
+                const double gv = g1 == 0u ? -CUDART_INF : (double)key_value(g1) + (g2 ? (double)key_value(g2) : 0.0);
+                int ahead = 0;
+                for (int j = 0; j < a.n_groups; ++j) {
+                    const double o = __shfl_sync(FULL, gv, j * every);
+                    ahead += o > gv || (o == gv && j < mine) ? 1 : 0;
+                }
+                kept = mine < a.n_groups && ahead < a.top_groups;
             }
-            const bool kept = mine < a.n_groups && ahead < a.top_groups;
+            groups = SCORED && near ? exact_groups<T, C>(a, row, lane, room) : __ballot_sync(FULL, kept);
             if (by_lane) {
+                kept = (groups >> lane) & 1u;
 #pragma unroll
                 for (int i = 0; i < C; ++i) key[i] = kept ? key[i] : 0u;
             } else {
-                const unsigned all = __ballot_sync(FULL, kept);
 #pragma unroll
                 for (int i = 0; i < C; ++i) {
                     const int e = lane * C + i;
-                    if (e < a.experts && !((all >> (e / gsize)) & 1u)) key[i] = 0u;
+                    if (e < a.experts && !((groups >> (e / gsize)) & 1u)) key[i] = 0u;
                 }
             }
         }
+        if (!SCORED && C > 1) {
 #pragma unroll
-        for (int i = 0; i < C; ++i) key[i] = key[i] ? (key[i] & ~LOW) | (LOW - i) : 0u;
+            for (int i = 0; i < C; ++i) key[i] = key[i] ? (key[i] & ~LOW) | (LOW - i) : 0u;
+        }
         sort_down<C>(key);
-        int id = -1;
-        uint32_t mine = 0u, next = 0u;                 // this lane's choice; the one behind the last
-        for (int it = 0; it <= a.top_k; ++it) {
+        // The top_k best, and behind them those too near the last to be told from it.
+        int id = -1, n = 0;
+        uint32_t mine = 0u, last = 0u;                 // this lane's candidate; the top_k-th
+        bool lost = false;                             // candidates beyond the warp's lanes
+        for (;; ++n) {
             const uint32_t head = key[0] & ~LOW, m = __reduce_max_sync(FULL, head);
             if (m == 0u) break;
-            if (it == a.top_k) { next = m; break; }
+            if (n >= a.top_k && !too_near<T, C, SCORED>(last, m)) break;
+            if (n == 32) { lost = true; break; }
+            if (n == a.top_k - 1) last = m;
             const int w = __ffs(__ballot_sync(FULL, head == m)) - 1;
             const int e = __shfl_sync(FULL, lane * C + (int)(LOW - (key[0] & LOW)), w);
-            if (lane == it) { id = e; mine = m; }
+            if (lane == n) { id = e; mine = m; }
             if (lane == w) {
 #pragma unroll
                 for (int i = 0; i + 1 < C; ++i) key[i] = key[i + 1];
@@ -300,15 +423,10 @@ __global__ void __launch_bounds__(128) k_moe_route(const RouteArgs a) {
             }
         }
         if (SCORED || std::is_same<T, float>::value) {
-            uint32_t behind = __shfl_down_sync(FULL, mine, 1);
-            if (lane == a.top_k - 1) behind = next;
-            if (lane < a.top_k && mine && behind) {
-                const float v = key_value(mine);
-                // (written so that infinities count as near)
-                if (SCORED) unsure |= !(v - key_value(behind) > (0x1p-18f + C * 0x1p-22f) * fmaxf(1.0f, fabsf(v)));
-                else unsure |= mine == behind && C > 1;
-            }
-            if (__any_sync(FULL, unsure)) id = route_exact<T>(a, row, lane, room);
+            const uint32_t behind = __shfl_down_sync(FULL, mine, 1);
+            const bool unsure = lane < n - 1 && too_near<T, C, SCORED>(mine, behind);
+            if (__any_sync(FULL, unsure || lost))
+                id = lost ? route_exact<T, C>(a, row, lane, groups) : exact_order<T, C>(a, row, lane, id, n, room);
         }
         // Weights in f32; renormalised ones relative to the largest chosen, so
         // that small scores keep their ratios.
@@ -317,14 +435,15 @@ __global__ void __launch_bounds__(128) k_moe_route(const RouteArgs a) {
         float w;
         if (a.sigmoid || a.renorm) {
             const float low = a.sigmoid ? fminf(l, 0.0f) : l;
-            const float ref = a.renorm ? warp_max(low) : 0.0f;
+            const float ref = a.renorm ? key_value(__reduce_max_sync(FULL, order_key(low))) : 0.0f;
             w = there ? exp_diff(low, ref) : 0.0f;
-            if (a.sigmoid) w = w / (1.0f + expf(-fabsf(l)));         // sigmoid = exp(min(l, 0)) / (1 + exp(-|l|))
+            if (a.sigmoid) w = __fdividef(w, 1.0f + expf(-fabsf(l)));   // sigmoid = exp(min(l, 0)) / (1 + exp(-|l|))
             if (a.renorm) {
                 // Where f64 has no score left (exp(-746) is 0), there is nothing to share.
                 const bool none = a.sigmoid ? ref < -745.0f : ref - top < -745.0f;
-                const float sum = warp_sum(there ? w : 0.0f);
-                w = sum > 0.0f && !none ? w / sum : 0.0f;
+                float sum = there ? w : 0.0f;
+                for (int o = a.sum_lanes; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+                w = sum > 0.0f && !none ? __fdividef(w, sum) : 0.0f;
             }
         } else {
             w = there ? exp_diff(l, top) * inv : 0.0f;
@@ -460,9 +579,24 @@ cudaError_t by_width(const A& a, cudaStream_t st) {
     if (c <= 16) return L<T, 16>::go(a, st);
     return L<T, 32>::go(a, st);
 }
-unsigned warp_grid(int64_t tokens, int per_sm) {
-    const int64_t need = (tokens + 3) / 4, most = (int64_t)sm_count() * per_sm;
-    return (unsigned)(need < most ? need : most);
+// CTAs of four warps that run at one time, so that every warp gets the same
+// number of tokens (more CTAs than that would leave a ragged last round).
+template <class K>
+cudaError_t resident_ctas(K kern, size_t smem, int (&cache)[64], int64_t tokens, unsigned* grid) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorUnknown;
+    if (dev < 0 || dev >= 64) return cudaErrorNotSupported;
+    int n = __atomic_load_n(&cache[dev], __ATOMIC_ACQUIRE);
+    if (n == 0) {
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, 128, smem);
+        if (e != cudaSuccess) return e;
+        if (n < 1) n = 1;
+        n *= sm_count();
+        __atomic_store_n(&cache[dev], n, __ATOMIC_RELEASE);
+    }
+    const int64_t need = (tokens + 3) / 4, rounds = (need + n - 1) / n;
+    *grid = (unsigned)((need + rounds - 1) / rounds);
+    return cudaSuccess;
 }
 template <class T, int C>
 struct RouteLaunch {
@@ -472,8 +606,15 @@ struct RouteLaunch {
         const int gsize = a.experts / a.n_groups, lanes = gsize / C;
         a.group_lanes = gsize % C == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
         const size_t smem = 4 * sizeof(double) * (size_t)a.experts;
-        if (a.bias) k_moe_route<T, C, true><<<warp_grid(a.tokens, 16), 128, smem, st>>>(a);
-        else k_moe_route<T, C, false><<<warp_grid(a.tokens, 16), 128, smem, st>>>(a);
+        // (by the shared memory of a full width: the cached count serves every call)
+        static int with_bias[64] = {0}, without[64] = {0};
+        unsigned grid = 0;
+        const size_t most = 4 * sizeof(double) * 32 * C;
+        const cudaError_t e = a.bias ? resident_ctas(k_moe_route<T, C, true>, most, with_bias, a.tokens, &grid)
+                                     : resident_ctas(k_moe_route<T, C, false>, most, without, a.tokens, &grid);
+        if (e != cudaSuccess) return e;
+        if (a.bias) k_moe_route<T, C, true><<<grid, 128, smem, st>>>(a);
+        else k_moe_route<T, C, false><<<grid, 128, smem, st>>>(a);
         return cudaGetLastError();
     }
 };
@@ -482,7 +623,11 @@ struct RouteBwdLaunch {
     static cudaError_t go(RouteBwdArgs a, cudaStream_t st) {
         constexpr int VEC = Traits<T>::VEC;
         a.vec = a.experts % VEC == 0 && ((uintptr_t)a.logits & 15u) == 0 && ((uintptr_t)a.dlogits & 15u) == 0;
-        k_moe_route_bwd<T, C><<<warp_grid(a.tokens, 16), 128, 0, st>>>(a);
+        static int ctas[64] = {0};
+        unsigned grid = 0;
+        const cudaError_t e = resident_ctas(k_moe_route_bwd<T, C>, 0, ctas, a.tokens, &grid);
+        if (e != cudaSuccess) return e;
+        k_moe_route_bwd<T, C><<<grid, 128, 0, st>>>(a);
         return cudaGetLastError();
     }
 };
@@ -912,7 +1057,8 @@ extern "C" bq_status bq_moe_route(const void* logits, bq_dtype dtype, int64_t to
     if (misaligned(logits, type_mask(dtype)) || misaligned(bias, 3) || misaligned(ids, 3) || misaligned(weights, 3))
         return BQ_ERR_MISALIGNED;
     RouteArgs a{logits, bias, tokens, experts, top_k, n_groups, top_groups, group_top, score == BQ_SCORE_SIGMOID,
-                renormalize != 0, 0, 0, scale, ids, weights};
+                renormalize != 0, 0, 0, 0, scale, ids, weights};
+    while (2 * a.sum_lanes < top_k) a.sum_lanes = a.sum_lanes ? 2 * a.sum_lanes : 1;
     cudaStream_t st = (cudaStream_t)stream;
     if (dtype == BQ_F32) return from(by_width<float, RouteLaunch>(a, st));
     if (dtype == BQ_F16) return from(by_width<__half, RouteLaunch>(a, st));

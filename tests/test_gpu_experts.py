@@ -418,3 +418,72 @@ def test_layer_in_a_graph_and_on_streams(bq):
             outs.append(run(x, logits))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
+
+
+def test_grouped_positions_past_the_activations(bq):
+    """Without rows a position is its activation row: those past the last count as zeros (their bias stays)."""
+    g = torch.Generator().manual_seed(16)
+    a, sa = codes((50, 256), g, 1)
+    w, sw = codes((2, 256, 256), g, 128)
+    bias = torch.randn((2, 256), generator=g).cuda()
+    for p in (70, 300):
+        off = torch.tensor([0, 20, p], dtype=torch.int32, device="cuda")
+        out = bq.api.fp8_grouped_gemm(a, sa, off, w, sw, None, bias, out=torch.empty((p, 256), device="cuda"))
+        ref = bq.api.fp8_grouped_gemm(a, sa, torch.tensor([0, 20, 50], dtype=torch.int32, device="cuda"), w, sw, None, bias, out_dtype=F32)
+        assert torch.equal(out[:50], ref) and torch.equal(out[50:], bias[1].expand(p - 50, 256))
+
+
+@pytest.mark.parametrize("m,n,k", [(16, 7168, 2048), (100, 4096, 1152), (3, 2048, 1024), (40, 128, 512), (130, 1000, 640), (128, 136, 5120)])
+def test_epilogue_shared_tiles(bq, m, n, k):
+    """Products of few tiles, whose k-blocks two or four CTAs share; the same bits every time."""
+    g = torch.Generator().manual_seed(m * n)
+    a, sa = codes((m, k), g, 1)
+    w, sw = codes((n, k), g, 128)
+    bias = torch.randn(n, generator=g).cuda()
+    res = torch.randn((m, n), generator=g).cuda()
+    z, d = product(values(a, sa, 1), values(w, sw, 128), k // 128)
+    # Up to four partial sums are joined: three more roundings of sums no larger than the bound's T / 2^-16.
+    z = z + bias.double()
+    d = d * (1 + 2.0 ** -6) + 2.0 ** -24 * (z.abs() + d)
+    v, dv = after_act(z, d, "gelu_tanh")
+    v = v + res.double()
+    dv = dv + 2.0 ** -24 * (v.abs() + dv)
+    got = bq.api.fp8_block_gemm_epilogue(a, sa, w, sw, bias, "gelu_tanh", res, F32)
+    bound_check(got, v, dv, F32, f"{m}x{n}x{k}")
+    for _ in range(3):
+        assert torch.equal(bq.api.fp8_block_gemm_epilogue(a, sa, w, sw, bias, "gelu_tanh", res, F32), got)
+
+
+def test_products_of_unaligned_scales_and_odd_k_blocks(bq):
+    """Scales that do not start on 16 bytes, and numbers of k-blocks that are no multiple of the stages'."""
+    g = torch.Generator().manual_seed(18)
+    for k in (128, 384, 640, 896, 1152):
+        for m, n in ((5, 300), (200, 4096), (1500, 1600)):
+            a, sa = codes((m, k), g, 1)
+            w, sw = codes((n, k), g, 128)
+            off = lambda t: torch.cat([t.new_zeros(1), t.reshape(-1)])[1:].view(t.shape)   # noqa: E731
+            want = bq.api.fp8_block_gemm_epilogue(a, sa, w, sw, None, "silu")
+            assert torch.equal(bq.api.fp8_block_gemm_epilogue(a, off(sa), w, off(sw), None, "silu"), want)
+            z, d = product(values(a, sa, 1), values(w, sw, 128), k // 128)
+            bound_check(want, *after_act(z, d * (1 + 2.0 ** -6), "silu"), BF, f"{m}x{n}x{k}")
+
+
+def test_training_step_of_a_dense_layer(bq):
+    """Forward with the kept value before the activation, its gradient, and the product of the gradient's codes with the
+    transposed weight: against the same steps in 64 bits on the same codes."""
+    g = torch.Generator().manual_seed(19)
+    m, n, k = 300, 512, 384
+    a, sa = codes((m, k), g, 1)
+    w, sw = codes((n, k), g, 128)
+    bias = (0.1 * torch.randn(n, generator=g)).cuda()
+    c, pre = bq.api.fp8_block_gemm_epilogue(a, sa, w, sw, bias, "gelu", out_dtype=BF, save_pre=True)
+    dy = torch.randn((m, n), generator=g).bfloat16().cuda()
+    dz, db = bq.api.gemm_epilogue_backward(dy, pre, "gelu")
+    z = pre.double().requires_grad_(True)
+    act64(z, "gelu").backward(dy.double())
+    assert ((db.double() - z.grad.sum(0)).abs() <= (2.0 ** -18 + m * 2.0 ** -24) * (dy.double().abs() * (2 + pre.double().abs())).sum(0)).all()
+    ez, sz = bq.api.fp8_block_quantize(dz, 1, 128)
+    wt, swt = w.t().contiguous(), sw.t().contiguous()
+    da = bq.api.fp8_block_gemm_epilogue(ez, sz, wt, swt, out_dtype=F32)
+    ref, err = product(values(ez, sz, 1), values(wt, swt, 128), n // 128)
+    bound_check(da, ref, err * (1 + 2.0 ** -6), F32, "da")

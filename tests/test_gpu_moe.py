@@ -367,3 +367,22 @@ def test_unaligned_rows(bq):
     named = pos[(pos >= 0) & (pos < y.shape[0])].long().cuda()
     assert torch.equal(a[named], c[named])
     assert ((b - d).abs() <= 2 * 128 * U * 128 * 16).all()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("e,ng,tg", [(256, 1, 1), (256, 8, 3), (60, 5, 2), (1024, 32, 9), (40, 1, 1)])
+def test_route_clusters_of_near_values(bq, score, dtype, e, ng, tg):
+    """Values in clusters far nearer than f32 scores can tell, of a few, of dozens and of more than a warp has lanes, astride
+    the last place chosen; the same for groups' sums."""
+    g = gen(e + ng)
+    x = torch.randn((60, e), generator=g)
+    for r in range(60):
+        some = torch.randperm(e, generator=g)[:(3, 12, 30, min(e, 50))[r % 4]]
+        x[r, some] = 3.0 + (1e-7 if r % 8 < 4 else 3e-6) * torch.randn(some.numel(), generator=g)
+    bias = 1e-7 * torch.randn(e, generator=g)
+    x = x.to(dtype)
+    for k in (1, 5, min(8, e), min(32, tg * e // ng)):
+        check_route(bq, x, k, bias, score, ng, tg, 2)
+        check_route(bq, x, k, None, score, ng, tg, 2)
+        check_route(bq, x, k, bias, score, ng, tg, 1)
