@@ -25,8 +25,7 @@ struct EpiArgs {
     int64_t n;              // columns of the product
     int64_t n_out;          // columns of c: n, gated n / 2
     int bias_t, c_t, act;
-    int vec;                // n_out a multiple of 8: vectors of eight columns
-    int bias_vec;           // the same of the bias, which also starts on 16 bytes
+    int bias_vec;           // eight biases in 16-byte loads: n a multiple of 8, the start on 16 bytes
 };
 [[maybe_unused]] EpiArgs make_epi(int64_t n, int64_t n_out, const void* bias, int bias_t, int act, const void* residual, void* c,
                                   int c_t, void* pre) {
@@ -34,7 +33,6 @@ struct EpiArgs {
     g.bias = bias; g.residual = residual; g.c = c; g.pre = pre;
     g.n = n; g.n_out = n_out;
     g.bias_t = bias_t; g.c_t = c_t; g.act = act;
-    g.vec = n_out % 8 == 0;
     g.bias_vec = n % 8 == 0 && ((uintptr_t)bias & 15u) == 0;
     return g;
 }
@@ -95,11 +93,6 @@ __device__ __forceinline__ void epi_store8(void* p, int t, int64_t i, const floa
         st16(reinterpret_cast<__nv_bfloat16*>(p) + i, pack_vec<__nv_bfloat16>(v));
     }
 }
-__device__ __forceinline__ void epi_store(void* p, int t, int64_t i, float v) {
-    if (t == BQ_F32) reinterpret_cast<float*>(p)[i] = v;
-    else if (t == BQ_F16) reinterpret_cast<__half*>(p)[i] = __float2half_rn(v);
-    else reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-}
 template <int ACT, int N>
 __device__ __forceinline__ void act_all(float (&z)[N][8]) {
 #pragma unroll
@@ -115,15 +108,6 @@ __device__ __forceinline__ void epi_act(int act, float (&z)[N][8]) {
         case BQ_ACT_GELU_TANH: act_all<BQ_ACT_GELU_TANH>(z); break;
         case BQ_ACT_SILU: act_all<BQ_ACT_SILU>(z); break;
         default: break;
-    }
-}
-__device__ __forceinline__ float epi_act1(int act, float z) {
-    switch (act) {
-        case BQ_ACT_RELU: return act_value<BQ_ACT_RELU>(z);
-        case BQ_ACT_GELU: return act_value<BQ_ACT_GELU>(z);
-        case BQ_ACT_GELU_TANH: return act_value<BQ_ACT_GELU_TANH>(z);
-        case BQ_ACT_SILU: return act_value<BQ_ACT_SILU>(z);
-        default: return z;
     }
 }
 
@@ -144,20 +128,73 @@ __device__ __forceinline__ void epi_stage(float* stage, int lane, bool row_in, i
     }
 }
 
+// The chunk where rows of c do not start on 16 bytes: V columns of a lane (two
+// where the width is even), eight values in flight. In kernels of its own (FLAT):
+// beside the other form it would spill registers of the widest tiles' promotion.
+template <class T, int V, int ROW4>
+__device__ __forceinline__ void epi_flat(const EpiArgs& g, const float* stage, int lane, int64_t row0, int rows, int64_t col,
+                                         int64_t bias_at) {
+    constexpr int N = 8 / V, LANES = 32 / V;       // rows of a lane at a time; lanes along a row
+    using Pack = typename std::conditional<sizeof(T) * V == 8, uint2, typename std::conditional<sizeof(T) * V == 4, uint32_t, uint16_t>::type>::type;
+    const int c = V * (lane % LANES);
+    if (col + c >= g.n_out) return;
+    float b[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) b[v] = g.bias ? epi_load(g.bias, g.bias_t, bias_at + c + v) : 0.0f;
+    const int64_t first = row0 * g.n_out + col + c;
+    const T* res = reinterpret_cast<const T*>(g.residual);
+    auto put = [&](void* p, int64_t at, const float* v) {
+        Pack k;
+        T* t = reinterpret_cast<T*>(&k);
+#pragma unroll
+        for (int j = 0; j < V; ++j) t[j] = to_out<T>(v[j]);
+        *reinterpret_cast<Pack*>(reinterpret_cast<T*>(p) + at) = k;
+    };
+#pragma unroll 1
+    for (int r0 = lane / LANES; r0 < rows; r0 += 8) {     // (V rows of a warp a step, N steps)
+        Pack raw[N];
+        float z[1][8];
+        if (res) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (r0 + V * i < rows) raw[i] = *reinterpret_cast<const Pack*>(res + first + (r0 + V * i) * g.n_out);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int r = r0 + V * i;
+            const float* s = stage + r * 4 * ROW4 + 4 * ((c >> 2) ^ (r & 7)) + (c & 3);
+#pragma unroll
+            for (int v = 0; v < V; ++v) z[0][V * i + v] = r < 32 ? s[v] + b[v] : 0.0f;
+            if (g.pre && r < rows) put(g.pre, first + r * g.n_out, &z[0][V * i]);
+        }
+        epi_act(g.act, z);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (r0 + V * i >= rows) break;
+            if (res) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) z[0][V * i + v] += (float)reinterpret_cast<const T*>(&raw[i])[v];
+            }
+            put(g.c, first + (r0 + V * i) * g.n_out, &z[0][V * i]);
+        }
+    }
+}
+
 // One staged chunk of a warp, whose rows are row0 + 0 .. of c, `rows` of them.
 // Plain: the columns col .. col + 31. Gated: the gate's columns col .. col + 15,
 // then the other half's. bias_at: the place of column col in the bias array.
 // Rows of the staging block are ROW4 16-byte slots apart; a lane has ROWS rows in
 // flight, as its registers allow.
-template <bool GATED, int ROWS, int ROW4 = 8>
+template <bool GATED, bool FLAT, int ROWS, int ROW4>
 __device__ __forceinline__ void epi_chunk(const EpiArgs& g, const float* stage, int lane, int64_t row0, int rows, int64_t col,
                                           int64_t bias_at) {
     const float4* st = reinterpret_cast<const float4*>(stage);
     // Lanes along a row; ROWS rows of a lane at a time.
     constexpr int LANES = GATED ? 2 : 4, RSTEP = 32 / LANES, N = ROWS;
-    if (g.vec && (GATED || col + 32 <= g.n_out)) {
+    if constexpr (!FLAT) {
         const int c = lane % LANES;
         const int64_t j = col + 8 * c;
+        if (!GATED && j >= g.n_out) return;        // (gated widths are multiples of 128)
 #pragma unroll 1
         for (int r0 = lane / LANES; r0 < rows; r0 += N * RSTEP) {
             U4 res[N][2];
@@ -216,16 +253,17 @@ __device__ __forceinline__ void epi_chunk(const EpiArgs& g, const float* stage, 
                 if (r0 + i * RSTEP < rows) epi_store8(g.c, g.c_t, (row0 + r0 + i * RSTEP) * g.n_out + j, z[i]);
             }
         }
-    } else if (!GATED && col + lane < g.n_out) {
-        // Odd widths, and the last columns: a lane per column.
-        const float b = g.bias ? epi_load(g.bias, g.bias_t, bias_at + lane) : 0.0f;
-        for (int r = 0; r < rows; ++r) {
-            const int64_t at = (row0 + r) * g.n_out + col + lane;
-            float z = stage[r * 4 * ROW4 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)] + b;
-            if (g.pre) epi_store(g.pre, g.c_t, at, z);
-            z = epi_act1(g.act, z);
-            if (g.residual) z += epi_load(g.residual, g.c_t, at);
-            epi_store(g.c, g.c_t, at, z);
+    } else {
+        const bool even = g.n_out % 2 == 0;
+        if (g.c_t == BQ_F32) {
+            if (even) epi_flat<float, 2, ROW4>(g, stage, lane, row0, rows, col, bias_at);
+            else epi_flat<float, 1, ROW4>(g, stage, lane, row0, rows, col, bias_at);
+        } else if (g.c_t == BQ_F16) {
+            if (even) epi_flat<__half, 2, ROW4>(g, stage, lane, row0, rows, col, bias_at);
+            else epi_flat<__half, 1, ROW4>(g, stage, lane, row0, rows, col, bias_at);
+        } else {
+            if (even) epi_flat<__nv_bfloat16, 2, ROW4>(g, stage, lane, row0, rows, col, bias_at);
+            else epi_flat<__nv_bfloat16, 1, ROW4>(g, stage, lane, row0, rows, col, bias_at);
         }
     }
 }
@@ -239,7 +277,7 @@ struct EpiPlan {
     static constexpr int COLS = SW == 64 ? 64 : 32;
     static constexpr uint32_t WARP_BYTES = 32 * COLS * 4;
 };
-template <int SW, bool GATED>
+template <int SW, bool GATED, bool FLAT>
 __device__ __forceinline__ void epi_tile(const EpiArgs& g, float* stage, int lane, int64_t row0, int rows, int64_t col,
                                          int64_t bias_at, bool row_in, const F2 (&acc)[SW]) {
     constexpr int COLS = EpiPlan<SW>::COLS, ROW4 = COLS / 4;      // staged columns
@@ -260,7 +298,7 @@ __device__ __forceinline__ void epi_tile(const EpiArgs& g, float* stage, int lan
         for (int c = 0; c < COLS / 32; ++c) {
             const int64_t at = col + (GATED ? 16 : 32) * (part * (COLS / 32) + c);
             if (at < g.n_out)                           // uniform over the warp
-                epi_chunk<GATED, GATED ? 1 : SW < 64 ? 2 : 4, ROW4>(g, stage + 32 * c, lane, row0, rows, at, bias_at + (at - col));
+                epi_chunk<GATED, FLAT, GATED ? 1 : SW < 64 ? 2 : 4, ROW4>(g, stage + 32 * c, lane, row0, rows, at, bias_at + (at - col));
         }
         __syncwarp();                                   // read before the next part is staged
     }

@@ -7,6 +7,7 @@
 // the same every time.
 #include "bq.h"
 #include "bq_act.cuh"
+#include "bq_cols.cuh"
 #include "bq_device.cuh"
 #include "bq_internal.h"
 
@@ -32,9 +33,13 @@ int64_t epi_splits(int64_t m, int64_t n) {
     return s < 1 ? 1 : s;
 }
 
+// V columns of a thread: 16 bytes where rows start on them, else two or one, with
+// as many more rows in flight.
 template <class T, int ACT, int V>
 __global__ void __launch_bounds__(EB_COLS* EB_ROWS) k_epi_bwd(const EpiBwdArgs a) {
     __shared__ float sum[EB_ROWS][EB_COLS * V + 1];
+    constexpr int R = V > 2 ? 2 : 8;             // (16 bytes: four rows leave fewer CTAs, 56 against 53 us at
+                                                 // 4096 x 11008 bf16, gelu_tanh; one: 72)
     const int cx = threadIdx.x % EB_COLS, ry = threadIdx.x / EB_COLS;
     const int64_t col = ((int64_t)blockIdx.x * EB_COLS + cx) * V;
     const int64_t r0 = (int64_t)blockIdx.y * a.rows_per, r1 = min(a.m, r0 + a.rows_per);
@@ -45,39 +50,29 @@ __global__ void __launch_bounds__(EB_COLS* EB_ROWS) k_epi_bwd(const EpiBwdArgs a
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
     if (col < a.n) {
-        // Two rows of a thread in flight (four: fewer CTAs fit, 56 against 53 us at
-        // 4096 x 11008 bf16, gelu_tanh; one: 72).
-        for (int64_t r = r0 + ry; r < r1; r += 2 * EB_ROWS) {
-            U4 gv[2], zv[2];
-            float g[V], z[V];
+        for (int64_t r = r0 + ry; r < r1; r += R * EB_ROWS) {
+            // dz may be dy itself: ordinary loads, before the stores below.
+            Cols<T, V> gv[R], zv[R];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int64_t at = (r + q * EB_ROWS) * a.n + col;
+            for (int q = 0; q < R; ++q) {
                 if (r + q * EB_ROWS >= r1) break;
-                if constexpr (V > 1) {
-                    zv[q] = ld16_stream(pre + at);
-                    // dz may be dy itself: an ordinary load, before the stores below.
-                    gv[q] = *reinterpret_cast<const U4*>(dy + at);
-                }
+                const int64_t at = (r + q * EB_ROWS) * a.n + col;
+                zv[q].load(pre + at);
+                gv[q].load(dy + at);
             }
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int64_t at = (r + q * EB_ROWS) * a.n + col;
+            for (int q = 0; q < R; ++q) {
                 if (r + q * EB_ROWS >= r1) break;
-                if constexpr (V > 1) {
-                    load_vec<T>(zv[q], z);
-                    load_vec<T>(gv[q], g);
-                } else {
-                    z[0] = ld1<T>(pre + at);
-                    g[0] = (float)dy[at];
-                }
+                float g[V], z[V];
+                gv[q].get(g);
+                zv[q].get(z);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     g[i] *= act_slope<ACT>(z[i]);
                     acc[i] += g[i];
                 }
-                if constexpr (V > 1) st16(dz + at, pack_vec<T>(g));
-                else dz[at] = to_out<T>(g[0]);
+                gv[q].set(g);
+                gv[q].store(dz + (r + q * EB_ROWS) * a.n + col);
             }
         }
     }
@@ -112,10 +107,12 @@ cudaError_t launch_epi_bwd(EpiBwdArgs a, float* dbias, cudaStream_t st) {
     const int64_t splits = epi_splits(a.m, a.n);
     a.rows_per = (a.m + splits - 1) / splits;
     constexpr int VEC = Traits<T>::VEC;
-    const bool vec = a.n % VEC == 0 && (((uintptr_t)a.dy | (uintptr_t)a.pre | (uintptr_t)a.dz) & 15u) == 0;
-    const int64_t wide = EB_COLS * (vec ? VEC : 1);
+    const uintptr_t starts = (uintptr_t)a.dy | (uintptr_t)a.pre | (uintptr_t)a.dz;
+    const int v = a.n % VEC == 0 && (starts & 15u) == 0 ? VEC : a.n % 2 == 0 && starts % (2 * sizeof(T)) == 0 ? 2 : 1;
+    const int64_t wide = EB_COLS * v;
     const dim3 grid((unsigned)((a.n + wide - 1) / wide), (unsigned)splits);
-    if (vec) k_epi_bwd<T, ACT, VEC><<<grid, EB_COLS * EB_ROWS, 0, st>>>(a);
+    if (v == VEC) k_epi_bwd<T, ACT, VEC><<<grid, EB_COLS * EB_ROWS, 0, st>>>(a);
+    else if (v == 2) k_epi_bwd<T, ACT, 2><<<grid, EB_COLS * EB_ROWS, 0, st>>>(a);
     else k_epi_bwd<T, ACT, 1><<<grid, EB_COLS * EB_ROWS, 0, st>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !dbias) return e;

@@ -202,7 +202,8 @@ __device__ __forceinline__ void promote_runs(F2 (&acc)[SW], uint32_t t0, uint32_
 // and the first adds up their sums (in the order of their ranks, through its
 // shared memory) and writes the tile: for products of few tiles, which would
 // otherwise leave most SMs idle.
-template <int BN, bool GATED, int XR, bool SPLIT>
+// FLAT: c's columns are not a multiple of 8 (see epi_flat).
+template <int BN, bool GATED, int XR, bool SPLIT, bool FLAT>
 __global__ void __launch_bounds__(X_NT, 1) k_fp8_experts(const __grid_constant__ CUtensorMap tm_a,
                                                          const __grid_constant__ CUtensorMap tm_w,
                                                          const __grid_constant__ ExpertArgs g) {
@@ -548,7 +549,7 @@ __global__ void __launch_bounds__(X_NT, 1) k_fp8_experts(const __grid_constant__
                 }
             }
             if (busy)
-                epi_tile<SW, GATED>(g.epi, stage, lane, t.p0 + 32 * q, mine_rows, col, (int64_t)t.e * g.n + col, row_in, acc);
+                epi_tile<SW, GATED, FLAT>(g.epi, stage, lane, t.p0 + 32 * q, mine_rows, col, (int64_t)t.e * g.n + col, row_in, acc);
         }
         if constexpr (SPLIT) {
             if (!joined) {                                       // gave up: the others still wait for this CTA
@@ -572,14 +573,14 @@ __global__ void __launch_bounds__(X_NT, 1) k_fp8_experts(const __grid_constant__
 }
 
 // `split`: CTAs of a cluster that share a tile (SPLIT kernels).
-template <int BN, bool GATED, int XR, bool SPLIT = false>
+template <int BN, bool GATED, int XR, bool SPLIT, bool FLAT>
 cudaError_t launch_experts(const uint8_t* w, const ExpertArgs& ga, cudaStream_t st, int split = 1) {
     using P = PlanX<BN, XR>;
     static int ready[64] = {0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorUnknown;
     if (dev < 0 || dev >= 64) return cudaErrorNotSupported;
-    auto kern = k_fp8_experts<BN, GATED, XR, SPLIT>;
+    auto kern = k_fp8_experts<BN, GATED, XR, SPLIT, FLAT>;
     cudaError_t e;
     if (!__atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE)) {
         cudaFuncAttributes fa;
@@ -625,12 +626,20 @@ cudaError_t launch_experts(const uint8_t* w, const ExpertArgs& ga, cudaStream_t 
 //   against 121), with tiles enough to fill the card twice;
 //   tiles of 32 rows up to 8 rows an expert (64 rows: 140 against 150; 256: 155
 //   against 162; 16 rows an expert of n 7168 k 2048: 120 against 117).
+//   Widths that are no multiple of 8 stay on 128 columns, whose promotion leaves
+//   room for their epilogue.
 template <bool GATED>
 cudaError_t launch_by_shape(const uint8_t* w, const ExpertArgs& g, cudaStream_t st) {
     const int64_t p = g.p, e = g.n_experts;
-    if (p <= 8 * e) return launch_experts<128, GATED, 32>(w, g, st);
-    if (p >= 128 * e && (p / XM) * ((g.n + 255) / 256) >= 2 * sm_count()) return launch_experts<256, GATED, 128>(w, g, st);
-    return launch_experts<128, GATED, 128>(w, g, st);
+    if constexpr (!GATED) {
+        if (g.n % 8 != 0)
+            return p <= 8 * e ? launch_experts<128, false, 32, false, true>(w, g, st)
+                              : launch_experts<128, false, 128, false, true>(w, g, st);
+    }
+    if (p <= 8 * e) return launch_experts<128, GATED, 32, false, false>(w, g, st);
+    if (p >= 128 * e && (p / XM) * ((g.n + 255) / 256) >= 2 * sm_count())
+        return launch_experts<256, GATED, 128, false, false>(w, g, st);
+    return launch_experts<128, GATED, 128, false, false>(w, g, st);
 }
 
 }  // namespace
@@ -665,10 +674,14 @@ cudaError_t fp8_dense(const uint8_t* a, const float* sa, int64_t m, int64_t k, c
     ExpertArgs g = make_args(a, sa, m, k, nullptr, nullptr, 1, m, sw, n);
     g.epi = make_epi(n, n, bias, bias_t, act, residual, c, c_t, pre);
     const int64_t tiles = ((m + XM - 1) / XM) * ((n + 127) / 128), sms = sm_count();
-    if (tiles > sms) return launch_experts<256, false, 128>(w, g, st);
-    if (4 * tiles <= sms && g.nkb >= 8) return launch_experts<128, false, 128, true>(w, g, st, 4);
-    if (2 * tiles <= sms && g.nkb >= 4) return launch_experts<128, false, 128, true>(w, g, st, 2);
-    return launch_experts<128, false, 128>(w, g, st);
+    const bool flat = n % 8 != 0;
+    if (tiles > sms)
+        return flat ? launch_experts<128, false, 128, false, true>(w, g, st) : launch_experts<256, false, 128, false, false>(w, g, st);
+    const int split = 4 * tiles <= sms && g.nkb >= 8 ? 4 : 2 * tiles <= sms && g.nkb >= 4 ? 2 : 1;
+    if (split > 1)
+        return flat ? launch_experts<128, false, 128, true, true>(w, g, st, split)
+                    : launch_experts<128, false, 128, true, false>(w, g, st, split);
+    return flat ? launch_experts<128, false, 128, false, true>(w, g, st) : launch_experts<128, false, 128, false, false>(w, g, st);
 }
 
 }  // namespace bq

@@ -6,6 +6,7 @@
 
 #include "bq.h"
 #include "bq_act.cuh"
+#include "bq_cols.cuh"
 #include "bq_device.cuh"
 #include "bq_internal.h"
 
@@ -817,73 +818,16 @@ struct CombineArgs {
     int top_k;
 };
 
-// V columns of a row, as they lie in memory until their values are needed.
-template <class T, int V>
-struct Cols {
-    static constexpr bool WIDE = V * sizeof(T) >= 16;
-    static constexpr int N = WIDE ? V * (int)sizeof(T) / 16 : V;
-    typename std::conditional<WIDE, U4, T>::type raw[N];
-    __device__ __forceinline__ void load(const T* p) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) raw[i] = reinterpret_cast<const typename std::conditional<WIDE, U4, T>::type*>(p)[i];
-    }
-    __device__ __forceinline__ void values(float (&v)[V]) const {
-        if constexpr (WIDE) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                float x[Traits<T>::VEC];
-                load_vec<T>(raw[i], x);
-#pragma unroll
-                for (int j = 0; j < Traits<T>::VEC; ++j) v[i * Traits<T>::VEC + j] = x[j];
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = (float)raw[i];
-        }
-    }
-};
-// V columns of a row as f32, and rounded from f32.
-template <class T, int V>
-__device__ __forceinline__ void load_cols(const T* p, float (&v)[V]) {
-    if constexpr (V * sizeof(T) >= 16) {
-        constexpr int N = Traits<T>::VEC;
-#pragma unroll
-        for (int i = 0; i < V; i += N) {
-            float x[N];
-            load_vec<T>(*reinterpret_cast<const U4*>(p + i), x);
-#pragma unroll
-            for (int j = 0; j < N; ++j) v[i + j] = x[j];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = (float)p[i];
-    }
-}
-template <class T, int V>
-__device__ __forceinline__ void store_cols(T* p, const float (&v)[V]) {
-    if constexpr (V * sizeof(T) >= 16) {
-        constexpr int N = Traits<T>::VEC;
-#pragma unroll
-        for (int i = 0; i < V; i += N) {
-            float x[N];
-#pragma unroll
-            for (int j = 0; j < N; ++j) x[j] = v[i + j];
-            st16(p + i, pack_vec<T>(x));
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = to_out<T>(v[i]);
-    }
-}
-
 // A CTA takes a token (blockIdx.y: a share of its columns) and walks its columns
 // with the slots' positions in registers, the rows of eight slots (f32: four) in
 // flight at a time: with a thread per vector of the output, the wait for its
-// positions before every load held 4096 x 8 x 7168 at 140 us.
-template <class TY, class TO, int V>
+// positions before every load held 4096 x 8 x 7168 at 140 us. A thread has U runs
+// of W columns: 8 in one where rows start on 16 bytes, else four of 2 or 1.
+template <class TY, class TO, int W, int U>
 __global__ void __launch_bounds__(128) k_moe_combine(const CombineArgs a) {
     constexpr int B = sizeof(TY) == 2 ? 8 : 4;
     const TO* res = reinterpret_cast<const TO*>(a.residual);
+    const int64_t run = (int64_t)blockDim.x * W;       // columns from one run of a thread to its next
     for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
         const int32_t* pos = a.pos + t * a.top_k;
         const float* weights = a.weights + t * a.top_k;
@@ -898,35 +842,54 @@ __global__ void __launch_bounds__(128) k_moe_combine(const CombineArgs a) {
             }
         };
         slots(0);
-        for (int64_t c = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * V; c < a.hidden; c += (int64_t)gridDim.y * blockDim.x * V) {
-            const TY* y = reinterpret_cast<const TY*>(a.y) + c;
-            float acc[V];
+        for (int64_t c0 = (int64_t)blockIdx.y * run * U + threadIdx.x * W; c0 < a.hidden; c0 += (int64_t)gridDim.y * run * U) {
+            float acc[U][W];
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-            Cols<TO, V> r;
-            if (res) r.load(res + t * a.hidden + c);
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < W; ++i) acc[u][i] = 0.0f;
+            Cols<TO, W> r[U];
+            if (res) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + u * run < a.hidden) r[u].load(res + t * a.hidden + c0 + u * run);
+            }
             for (int j0 = 0; j0 < a.top_k; j0 += B) {
                 if (a.top_k > B) slots(j0);
-                Cols<TY, V> v[B];
+                Cols<TY, W> v[B][U];
 #pragma unroll
-                for (int j = 0; j < B; ++j)
-                    if (p[j] >= 0) v[j].load(y + p[j] * a.hidden);
+                for (int j = 0; j < B; ++j) {
+                    if (p[j] < 0) continue;
+                    const TY* y = reinterpret_cast<const TY*>(a.y) + p[j] * a.hidden + c0;
 #pragma unroll
-                for (int j = 0; j < B; ++j)
-                    if (p[j] >= 0) {
-                        float x[V];
-                        v[j].values(x);
+                    for (int u = 0; u < U; ++u)
+                        if (u == 0 || c0 + u * run < a.hidden) v[j][u].load(y + u * run);
+                }
 #pragma unroll
-                        for (int i = 0; i < V; ++i) acc[i] = fmaf(w[j], x[i], acc[i]);
+                for (int j = 0; j < B; ++j) {
+                    if (p[j] < 0) continue;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        float x[W];
+                        v[j][u].get(x);
+#pragma unroll
+                        for (int i = 0; i < W; ++i) acc[u][i] = fmaf(w[j], x[i], acc[u][i]);
                     }
+                }
             }
-            if (res) {
-                float x[V];
-                r.values(x);
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] += x[i];
+            for (int u = 0; u < U; ++u) {
+                if (c0 + u * run >= a.hidden) break;
+                if (res) {
+                    float x[W];
+                    r[u].get(x);
+#pragma unroll
+                    for (int i = 0; i < W; ++i) acc[u][i] += x[i];
+                }
+                Cols<TO, W> o;
+                o.set(acc[u]);
+                o.store(reinterpret_cast<TO*>(a.out) + t * a.hidden + c0 + u * run);
             }
-            store_cols<TO, V>(reinterpret_cast<TO*>(a.out) + t * a.hidden + c, acc);
         }
     }
 }
@@ -942,7 +905,7 @@ struct CombineBwdArgs {
     int top_k;
 };
 
-template <class T, int V>
+template <class T, int W, int U>
 __global__ void __launch_bounds__(128) k_moe_combine_bwd(const CombineBwdArgs a) {
     __shared__ float part[32][4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -961,25 +924,39 @@ __global__ void __launch_bounds__(128) k_moe_combine_bwd(const CombineBwdArgs a)
                 if (p[j] >= a.y_rows) p[j] = -1;
                 dot[j] = 0.0f;
             }
-            for (int64_t c = (int64_t)threadIdx.x * V; c < a.hidden; c += 128 * V) {
-                float d[V];
-                Cols<T, V> y[B];
+            for (int64_t c0 = threadIdx.x * W; c0 < a.hidden; c0 += 128 * W * U) {
+                Cols<T, W> y[B][U], d[U];
 #pragma unroll
-                for (int j = 0; j < B; ++j)
-                    if (p[j] >= 0) y[j].load(reinterpret_cast<const T*>(a.y) + p[j] * a.hidden + c);
-                load_cols<T, V>(dout + c, d);
+                for (int j = 0; j < B; ++j) {
+                    if (p[j] < 0) continue;
+                    const T* from = reinterpret_cast<const T*>(a.y) + p[j] * a.hidden + c0;
 #pragma unroll
-                for (int j = 0; j < B; ++j)
-                    if (p[j] >= 0) {
-                        float x[V], o[V];
-                        y[j].values(x);
+                    for (int u = 0; u < U; ++u)
+                        if (u == 0 || c0 + 128 * W * u < a.hidden) y[j][u].load(from + 128 * W * u);
+                }
 #pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            dot[j] = fmaf(d[i], x[i], dot[j]);
-                            o[i] = w[j] * d[i];
+                for (int u = 0; u < U; ++u)
+                    if (u == 0 || c0 + 128 * W * u < a.hidden) d[u].load(dout + c0 + 128 * W * u);
+#pragma unroll
+                for (int j = 0; j < B; ++j) {
+                    if (p[j] < 0) continue;
+                    T* to = reinterpret_cast<T*>(a.dy) + p[j] * a.hidden + c0;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (u > 0 && c0 + 128 * W * u >= a.hidden) break;
+                        float g[W], x[W];
+                        d[u].get(g);
+                        y[j][u].get(x);
+#pragma unroll
+                        for (int i = 0; i < W; ++i) {
+                            dot[j] = fmaf(g[i], x[i], dot[j]);
+                            g[i] *= w[j];
                         }
-                        store_cols<T, V>(reinterpret_cast<T*>(a.dy) + p[j] * a.hidden + c, o);
+                        Cols<T, W> o;
+                        o.set(g);
+                        o.store(to + 128 * W * u);
                     }
+                }
             }
 #pragma unroll
             for (int j = 0; j < B; ++j) {
@@ -998,20 +975,32 @@ __global__ void __launch_bounds__(128) k_moe_combine_bwd(const CombineBwdArgs a)
     }
 }
 
-// Vectors of eight columns where a row's columns and the tensors' starts allow
-// 16-byte accesses. As many threads as a row has vectors, 128 at most; few tokens
-// get several CTAs each.
-template <class TY, class TO>
-cudaError_t launch_combine(const CombineArgs& a, cudaStream_t st) {
-    const bool vec = a.hidden % 8 == 0 && (((uintptr_t)a.y | (uintptr_t)a.residual | (uintptr_t)a.out) & 15u) == 0;
-    const int64_t per_row = vec ? a.hidden / 8 : a.hidden, sms = sm_count();
+// Columns of an access: eight where a row's columns and the tensors' starts allow
+// 16-byte ones, two where they are even, else one.
+int col_width(int64_t hidden, uintptr_t starts, size_t most) {
+    if (hidden % 8 == 0 && (starts & 15u) == 0) return 8;
+    return hidden % 2 == 0 && (starts & (2 * most - 1)) == 0 ? 2 : 1;
+}
+// As many threads as a row has accesses, 128 at most; few tokens get several CTAs
+// each.
+template <class TY, class TO, int W, int U>
+cudaError_t launch_combine_as(const CombineArgs& a, cudaStream_t st) {
+    const int64_t per_row = (a.hidden + W * U - 1) / (W * U), sms = sm_count();
     const unsigned threads = per_row >= 128 ? 128u : (unsigned)((per_row + 31) / 32 * 32);
     const int64_t shares = (per_row + threads - 1) / threads, want = (4 * sms + a.tokens - 1) / a.tokens;
     const int64_t gx = a.tokens < 16 * sms ? a.tokens : 16 * sms, gy = want < shares ? want : shares;
     const dim3 grid((unsigned)gx, (unsigned)(gy < 65535 ? gy : 65535));
-    if (vec) k_moe_combine<TY, TO, 8><<<grid, threads, 0, st>>>(a);
-    else k_moe_combine<TY, TO, 1><<<grid, threads, 0, st>>>(a);
+    k_moe_combine<TY, TO, W, U><<<grid, threads, 0, st>>>(a);
     return cudaGetLastError();
+}
+template <class TY, class TO>
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t st) {
+    const size_t most = sizeof(TY) > sizeof(TO) ? sizeof(TY) : sizeof(TO);
+    switch (col_width(a.hidden, (uintptr_t)a.y | (uintptr_t)a.residual | (uintptr_t)a.out, most)) {
+        case 8: return launch_combine_as<TY, TO, 8, 1>(a, st);
+        case 2: return launch_combine_as<TY, TO, 2, 4>(a, st);
+        default: return launch_combine_as<TY, TO, 1, 4>(a, st);
+    }
 }
 template <class TY>
 cudaError_t combine_out(const CombineArgs& a, bq_dtype out, cudaStream_t st) {
@@ -1021,11 +1010,13 @@ cudaError_t combine_out(const CombineArgs& a, bq_dtype out, cudaStream_t st) {
 }
 template <class T>
 cudaError_t launch_combine_bwd(const CombineBwdArgs& a, cudaStream_t st) {
-    const bool vec = a.hidden % 8 == 0 && (((uintptr_t)a.dout | (uintptr_t)a.y | (uintptr_t)a.dy) & 15u) == 0;
     const int64_t most = (int64_t)sm_count() * 16;
     const unsigned grid = (unsigned)(a.tokens < most ? a.tokens : most);
-    if (vec) k_moe_combine_bwd<T, 8><<<grid, 128, 0, st>>>(a);
-    else k_moe_combine_bwd<T, 1><<<grid, 128, 0, st>>>(a);
+    switch (col_width(a.hidden, (uintptr_t)a.dout | (uintptr_t)a.y | (uintptr_t)a.dy, sizeof(T))) {
+        case 8: k_moe_combine_bwd<T, 8, 1><<<grid, 128, 0, st>>>(a); break;
+        case 2: k_moe_combine_bwd<T, 2, 4><<<grid, 128, 0, st>>>(a); break;
+        default: k_moe_combine_bwd<T, 1, 4><<<grid, 128, 0, st>>>(a); break;
+    }
     return cudaGetLastError();
 }
 
