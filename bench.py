@@ -703,7 +703,7 @@ def run_reference(args):
 # something), prepared untimed, then the op launched `--ncu-reps` times.
 NCU_CASES = ("xpose", "nvfp4_quant", "nvfp4_deq", "mxfp8_quant", "mxfp8_deq", "mxfp4_quant",
              "fp8_1x128_quant", "fp8_block_deq", "tensor_amax", "fp8_tensor_store", "predeq_fp8",
-             "concat_rows", "gemm", "gemm_q")
+             "concat_rows", "gemm", "gemm_q", "gemm_epilogue", "experts", "experts_decode", "route", "combine")
 
 
 def ncu_case(name, reps):
@@ -767,6 +767,30 @@ def ncu_case(name, reps):
         ea, sa = A.fp8_block_quantize(a, 1, 128)
         ew, sw = A.fp8_block_quantize(w, 128, 128)
         fn = lambda: A.fp8_block_gemm_quantized(ea, sa, ew, sw)   # noqa: E731
+    elif name == "gemm_epilogue":
+        a = synthetic.device_tensor(st, (4096, K), "bf16")
+        w = synthetic.device_tensor(st, (9216, K), "bf16", std=0.05)
+        ea, sa = A.fp8_block_quantize(a, 1, 128)
+        ew, sw = A.fp8_block_quantize(w, 128, 128)
+        bias = synthetic.device_tensor(st, (9216,), "bf16")
+        fn = lambda: A.fp8_block_gemm_epilogue(ea, sa, ew, sw, bias, "gelu_tanh")   # noqa: E731
+    elif name in ("experts", "experts_decode"):
+        tokens, e, top_k = (2048, 8, 2) if name == "experts" else (32, 16, 2)
+        ea, sa = A.fp8_block_quantize(synthetic.device_tensor(st, (tokens, K), "bf16"), 1, 128)
+        ew, sw = A.fp8_block_quantize(synthetic.device_tensor(st, (e * 4096, K), "bf16", std=0.05), 128, 128)
+        ids, _ = A.moe_route(synthetic.device_tensor(st, (tokens, e), "f32"), top_k)
+        offsets, rows, _ = A.moe_group(ids, e)
+        ew, sw = ew.view(e, 4096, K), sw.view(e, 32, K // 128)
+        fn = lambda: A.fp8_grouped_gemm(ea, sa, offsets, ew, sw, rows, act="silu", gated=True)   # noqa: E731
+    elif name == "route":
+        x = synthetic.device_tensor(st, (16384, 256), "f32")
+        bias = synthetic.device_tensor(st, (256,), "f32", std=0.05)
+        fn = lambda: A.moe_route(x, 8, bias, "sigmoid", 8, 4)   # noqa: E731
+    elif name == "combine":
+        y = synthetic.device_tensor(st, (R, K), "bf16")
+        w = torch.full((R // 8, 8), 0.125, device=dev)
+        pos = torch.randperm(R, device=dev).to(torch.int32).view(R // 8, 8)
+        fn = lambda: A.moe_combine(y, pos, w)   # noqa: E731
     else:
         raise SystemExit(f"unknown case {name}")
     torch.cuda.synchronize()

@@ -635,7 +635,7 @@ struct RouteBwdLaunch {
 
 // ---------------------------------------------------------------- expert order
 // A stable counting sort of the pairs (token, slot) by expert in one launch:
-// the eight CTAs of a cluster take consecutive runs of the pairs, each warp a
+// the CTAs of a cluster (16, where the device allows that many) take consecutive runs of the pairs, each warp a
 // consecutive run of its CTA's. Pass one counts per warp and expert; prefix
 // sums over the warps, over the CTAs (through distributed shared memory) and
 // over the experts give every (warp, expert) its first position; pass two
@@ -644,7 +644,7 @@ struct RouteBwdLaunch {
 // number. The same result every time (only the counts use atomics).
 // Bound by latency: a run's ids are loaded GROUP_ROWS at a time, so that few
 // loads from memory follow one another, and kept where they are all.
-constexpr int GROUP_CTAS = 8, GROUP_NT = 1024, GROUP_WARPS = GROUP_NT / 32, GROUP_ROWS = 16;
+constexpr int GROUP_CTAS = 16, GROUP_NT = 1024, GROUP_WARPS = GROUP_NT / 32, GROUP_ROWS = 16;
 
 struct GroupArgs {
     const int32_t* ids;
@@ -773,20 +773,38 @@ __global__ void __launch_bounds__(GROUP_NT, 1) k_moe_group(const GroupArgs a) {
 
 cudaError_t launch_group(GroupArgs a, cudaStream_t st) {
     const size_t smem = ((size_t)GROUP_WARPS + 1) * a.n * sizeof(int32_t);
-    static int ready[64] = {0};
+    static int clusters[64] = {0};                      // CTAs of the largest cluster
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorUnknown;
     if (dev < 0 || dev >= 64) return cudaErrorNotSupported;
-    if (!__atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE)) {
-        const cudaError_t e = cudaFuncSetAttribute(k_moe_group, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (GROUP_WARPS + 1) * 1024 * (int)sizeof(int32_t));
+    int largest = __atomic_load_n(&clusters[dev], __ATOMIC_ACQUIRE);
+    if (largest == 0) {
+        cudaError_t e = cudaFuncSetAttribute(k_moe_group, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (GROUP_WARPS + 1) * 1024 * (int)sizeof(int32_t));
         if (e != cudaSuccess) return e;
-        __atomic_store_n(&ready[dev], 1, __ATOMIC_RELEASE);
+        largest = 8;
+        if (cudaFuncSetAttribute(k_moe_group, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+            cudaLaunchConfig_t probe = {};
+            cudaLaunchAttribute size[1];
+            size[0].id = cudaLaunchAttributeClusterDimension;
+            size[0].val.clusterDim.x = GROUP_CTAS;
+            size[0].val.clusterDim.y = 1;
+            size[0].val.clusterDim.z = 1;
+            probe.gridDim = dim3(GROUP_CTAS);
+            probe.blockDim = dim3(GROUP_NT);
+            probe.dynamicSmemBytes = (GROUP_WARPS + 1) * 1024 * sizeof(int32_t);
+            probe.attrs = size;
+            probe.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, k_moe_group, &probe) == cudaSuccess && n > 0) largest = GROUP_CTAS;
+        }
+        (void)cudaGetLastError();
+        __atomic_store_n(&clusters[dev], largest, __ATOMIC_RELEASE);
     }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     // One CTA alone while its warps have four rows of pairs at most.
-    const unsigned ctas = a.pairs > 4 * GROUP_NT ? GROUP_CTAS : 1;
+    const unsigned ctas = a.pairs > 4 * GROUP_NT ? (unsigned)largest : 1u;
     a.per = (int)(((int64_t)a.pairs + (int64_t)ctas * GROUP_NT - 1) / ((int64_t)ctas * GROUP_NT)) * 32;
     a.bits = 1;
     while ((a.n >> a.bits) != 0) ++a.bits;
