@@ -5,14 +5,15 @@
 //   S = sum over the 128 k of block b of dec(a[r, k]) dec(w[e, j, k]),
 // for the positions p of expert e, with r = rows[p] or p.
 //
-// One CTA per SM works through tiles of 128 positions x BN columns, an expert's
+// One CTA per SM works through tiles of XR positions x BN columns, an expert's
 // row tiles next to each other for each of its weight panels, so that a panel
 // is read from HBM once. A tile that reaches past an expert's last row computes
 // rows that are not stored. Per k-block of 128:
 //   warps 0, 3  the tile's activation rows: in place by TMA in boxes of 32 rows
 //               (warp 0), by index with 16-byte asynchronous copies (both warps:
 //               TMA's gather of four rows took 37 ns an instruction, 1.2 us per
-//               k-block of 128 rows); only as many rows as the tile has;
+//               k-block of 128 rows); only as many rows as the tile has. On the
+//               widest tiles warp 3 also copies the block scales;
 //   warp 1      TMA: BN weight rows in two boxes (gated: the first half from
 //               the gate's rows, the second from the other half's);
 //   warp 2      tcgen05.mma.kind::f8f6f4 (M 128, N BN, K 32) into a ring of
@@ -22,6 +23,13 @@
 //               so that a thread holds both factors of its results).
 // The scales are f32 and differ per k-block, so each k-block's partial has to
 // leave TMEM; warps whose 32 rows all lie past the tile's last row skip that.
+//
+// What bounds it. Long runs of rows: the promotion's reads of TMEM beside the
+// MMA's own (tensor pipe 47-51 % active; 16384 x 4096 x 7168 without extras 463
+// us, 2.08 PFLOP/s). Its loop has to keep two loads of 32 columns in flight and
+// spill nothing: with one load 750 us, with 100 bytes of spills 670. Few rows:
+// the weights' stream from HBM (64 rows on 32 experts of 4096 x 7168: 141 us,
+// 5.8 TB/s, 0.89 of the copy rate).
 #include "bq.h"
 #include "bq_device.cuh"
 #include "bq_epi.cuh"

@@ -573,8 +573,11 @@ typedef enum bq_act {
  *   c        [m, n] F32, F16 or BF16 (c_dtype), 16-byte aligned, overwritten;
  *   pre      [m, n] of c's dtype, 16-byte aligned, or NULL: the value before
  *            the activation, which bq_gemm_epilogue_backward takes.
- * Shape rules, errors and accuracy of P as there (P + bias, the activation and
- * the sum with the residual add a few f32 roundings). One launch. */
+ * Shape rules, errors and accuracy of P as there, with m, n, k < 2^31 - 256 (P +
+ * bias, the activation and the sum with the residual add a few f32 roundings).
+ * One launch. A product of few tiles is shared by two or four CTAs per tile,
+ * whose sums over their k-blocks are joined in a fixed order: the same bits
+ * every time, but not always those of bq_fp8_block_gemm_quantized. */
 bq_status bq_fp8_block_gemm_epilogue(const uint8_t* a_e4m3, const float* a_scale, int64_t m, int64_t k,
                                      const uint8_t* w_e4m3, const float* w_scale, int64_t n,
                                      const void* bias, bq_dtype bias_dtype, bq_act act,
