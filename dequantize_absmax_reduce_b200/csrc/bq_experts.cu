@@ -465,6 +465,14 @@ __global__ void __launch_bounds__(X_NT, 1) k_fp8_experts(const __grid_constant__
                 if (ar >= g.a_rows) ar = -1;
             }
             const bool row_in = ar >= 0, use = row_in && col < g.n;
+            if constexpr (!GATED) {
+                // The biases into the first level cache, where the epilogue finds them
+                // (1999 rows, 32 experts, n 7168, k 2048: 120.5 -> 116 us).
+                const int es = g.epi.bias_t == BQ_F32 ? 4 : 2, at = lane * (128 / es);
+                if (busy && g.epi.bias && at < 2 * SW && col + at < g.n)
+                    asm volatile("prefetch.global.L1 [%0];"
+                                 :: "l"(reinterpret_cast<const char*>(g.epi.bias) + ((int64_t)t.e * g.n + col + at) * es));
+            }
             const float* sap = g.sa + (int64_t)max(ar, 0) * nkb;
             const float* swp = g.sw + ((int64_t)t.e * g.nsw + (use ? col / 128 : 0)) * nkb;
             const int up = GATED ? (int)(g.n / 256) * nkb : 0;   // from a gate's scales to the other half's

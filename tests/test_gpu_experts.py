@@ -487,3 +487,77 @@ def test_training_step_of_a_dense_layer(bq):
     da = bq.api.fp8_block_gemm_epilogue(ez, sz, wt, swt, out_dtype=F32)
     ref, err = product(values(ez, sz, 1), values(wt, swt, 128), n // 128)
     bound_check(da, ref, err * (1 + 2.0 ** -6), F32, "da")
+
+
+def test_layer_of_no_tokens_and_of_no_local_expert(bq):
+    g = torch.Generator().manual_seed(20)
+    w1, s1 = codes((4, 512, 256), g, 128)
+    w2, s2 = codes((4, 256, 256), g, 128)
+    none = bq.api.fp8_moe(torch.empty((0, 256), dtype=BF, device="cuda"), torch.empty((0, 16), device="cuda"), w1, s1, w2, s2, 2)
+    assert none.shape == (0, 256)
+    x = torch.randn((9, 256), generator=g).bfloat16().cuda()
+    logits = torch.full((9, 16), -5.0)
+    logits[:, :4] = torch.randn((9, 4), generator=g)          # every choice is one of the first four experts
+    res = torch.randn((9, 256), generator=g).bfloat16().cuda()
+    out = bq.api.fp8_moe(x, logits.cuda(), w1, s1, w2, s2, 2, first_expert=8, residual=res)
+    assert torch.equal(out, res)
+
+
+def test_products_past_2_31_elements(bq):
+    """Offsets of c, of the epilogue's tensors and of gathered rows that pass 32 bits: the last rows against a small call."""
+    g = torch.Generator().manual_seed(21)
+    p, n, k = 290_000, 8192, 128                              # c: 2.4e9 elements
+    a, sa = codes((64, k), g, 1)
+    w, sw = codes((2, n, k), g, 128)
+    rows = (torch.arange(p, dtype=torch.int32) % 64).cuda()
+    off = torch.tensor([0, 5, p], dtype=torch.int32, device="cuda")
+    c = bq.api.fp8_grouped_gemm(a, sa, off, w, sw, rows, act="silu", out_dtype=BF)
+    tail = bq.api.fp8_grouped_gemm(a, sa, torch.tensor([0, 0, 600], dtype=torch.int32, device="cuda"), w, sw, rows[-600:].contiguous(), act="silu")
+    assert torch.equal(c[-600:], tail) and torch.equal(c[5 + 64 * 1000:5 + 64 * 1000 + 64], c[5:69])
+    dz, db = bq.api.gemm_epilogue_backward(c, c, "silu")
+    small, _ = bq.api.gemm_epilogue_backward(c[-600:].contiguous(), c[-600:].contiguous(), "silu")
+    assert torch.equal(dz[-600:], small) and torch.isfinite(db).all()
+
+
+def test_dense_product_past_2_31_elements(bq):
+    g = torch.Generator().manual_seed(22)
+    m, n, k = 290_000, 8192, 128
+    a, sa = codes((m, k), g, 1)
+    w, sw = codes((n, k), g, 128)
+    bias = torch.randn(n, generator=g).cuda()
+    c = bq.api.fp8_block_gemm_epilogue(a, sa, w, sw, bias, "relu", out_dtype=BF)
+    tail = bq.api.fp8_block_gemm_epilogue(a[-1000:].contiguous(), sa[-1000:].contiguous(), w, sw, bias, "relu", out_dtype=BF)
+    assert torch.equal(c[-1000:], tail)
+
+
+@pytest.mark.parametrize("counts", [[1, 0, 2], [5], [0, 3, 1, 1, 8, 0, 2, 9]])
+@pytest.mark.parametrize("n", [1, 37, 130, 259])
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_few_rows_odd_widths(bq, counts, n, gather):
+    """Tiles of 32 rows in the form for widths that are no multiple of 8."""
+    g = torch.Generator().manual_seed(n)
+    off, offsets = offsets_of(counts)
+    p = off[-1]
+    a, sa = codes((p, 640), g, 1)
+    w, sw = codes((len(counts), n, 640), g, 128)
+    rows = torch.randint(0, p, (p,), generator=g).to(torch.int32).cuda() if gather else None
+    bias = torch.randn((len(counts), n), generator=g).to(HF).cuda()
+    for out in (BF, HF, F32):
+        c = bq.api.fp8_grouped_gemm(a, sa, offsets, w, sw, rows, bias, "silu", out_dtype=out)
+        bound_check(c, *grouped_ref(a, sa, rows, off, w, sw, bias, "silu", False), out, f"{n}")
+
+
+@pytest.mark.parametrize("m,n,k", [(7, 361, 1152), (100, 129, 2048), (1, 2047, 1024), (128, 1022, 3200)])
+def test_epilogue_shared_tiles_odd_widths(bq, m, n, k):
+    g = torch.Generator().manual_seed(m + n)
+    a, sa = codes((m, k), g, 1)
+    w, sw = codes((n, k), g, 128)
+    res = torch.randn((m, n), generator=g).to(HF).cuda()
+    bias = torch.randn(n, generator=g).to(BF).cuda()
+    z, d = product(values(a, sa, 1), values(w, sw, 128), k // 128)
+    z = z + bias.double()
+    d = d * (1 + 2.0 ** -6) + 2.0 ** -24 * (z.abs() + d)       # as in test_epilogue_shared_tiles
+    v, dv = after_act(z, d, "silu")
+    got, pre = bq.api.fp8_block_gemm_epilogue(a, sa, w, sw, bias, "silu", res, HF, True)
+    bound_check(pre, z, d, HF, "pre")
+    bound_check(got, v + res.double(), dv + 2.0 ** -24 * ((v + res.double()).abs() + dv), HF, f"{m}x{n}x{k}")

@@ -386,3 +386,54 @@ def test_route_clusters_of_near_values(bq, score, dtype, e, ng, tg):
         check_route(bq, x, k, bias, score, ng, tg, 2)
         check_route(bq, x, k, None, score, ng, tg, 2)
         check_route(bq, x, k, bias, score, ng, tg, 1)
+
+
+def test_combine_without_rows(bq):
+    """No expert's row is here: the residual alone, gradients of zero."""
+    y = torch.empty((0, 40), dtype=torch.bfloat16, device="cuda")
+    pos = torch.tensor([[-1, 0], [3, -1]], dtype=torch.int32, device="cuda")
+    w = torch.ones((2, 2), device="cuda")
+    res = torch.randn((2, 40), device="cuda").bfloat16()
+    assert torch.equal(bq.api.moe_combine(y, pos, w, res), res)
+    assert (bq.api.moe_combine(y, pos, w) == 0).all()
+    dy, dw = bq.api.moe_combine_backward(res, y, pos, w)
+    assert dy.shape == (0, 40) and (dw == 0).all()
+
+
+def test_past_2_31_elements(bq):
+    """Rows of y, dy and logits whose offsets pass 32 bits, against small calls on the same rows."""
+    p, h = 290_000, 8192
+    y = torch.randn((64, h), generator=gen(1)).bfloat16().cuda().repeat(p // 64 + 1, 1)[:p].contiguous()
+    pos = torch.tensor([[p - 1, 0, p - 2], [p - 3, p - 4, -1]], dtype=torch.int32, device="cuda")
+    w = torch.rand((2, 3), generator=gen(2)).cuda()
+    at = pos.clamp_min(0).long()
+    few, few_pos = y[at.reshape(-1)], torch.arange(6, dtype=torch.int32, device="cuda").reshape(2, 3).where(pos >= 0, -1)
+    assert torch.equal(bq.api.moe_combine(y, pos, w), bq.api.moe_combine(few, few_pos, w))
+    dout = torch.randn((2, h), generator=gen(3)).bfloat16().cuda()
+    dy, dw = bq.api.moe_combine_backward(dout, y, pos, w)
+    dy2, dw2 = bq.api.moe_combine_backward(dout, few, few_pos, w)
+    named = pos >= 0
+    assert torch.equal(dw, dw2) and torch.equal(dy[pos[named].long()], dy2[few_pos[named].long()])
+    del y, dy
+    t, e = 2_200_000, 1024
+    x = torch.randn((4096, e), generator=gen(4)).bfloat16().cuda().repeat(t // 4096 + 1, 1)[:t].contiguous()
+    ids, wt = bq.api.moe_route(x, 4)
+    i2, w2 = bq.api.moe_route(x[-5000:].contiguous(), 4)
+    assert torch.equal(ids[-5000:], i2) and torch.equal(wt[-5000:], w2)
+    dx = bq.api.moe_route_backward(x, ids, wt, renormalize=False)
+    assert torch.equal(dx[-5000:], bq.api.moe_route_backward(x[-5000:].contiguous(), i2, w2, renormalize=False))
+
+
+def test_order_of_many_pairs(bq):
+    """More pairs than the warps of a cluster hold at once; many equal ids."""
+    ids = torch.randint(-2, 70, (400_000, 6), generator=gen(5)).to(torch.int32)
+    off, rows, pos = (v.cpu() for v in bq.api.moe_group(ids.cuda(), 64))
+    flat = ids.reshape(-1).long()
+    key = torch.where((flat >= 0) & (flat < 64), flat, 64)
+    order = torch.argsort(key, stable=True)
+    n = int((key < 64).sum())
+    assert off.tolist() == [0] + torch.bincount(key, minlength=65)[:64].cumsum(0).tolist()
+    assert torch.equal(rows[:n].long(), order[:n] // 6) and (rows[n:] == -1).all()
+    rank = torch.full_like(order, -1)
+    rank[order[:n]] = torch.arange(n)
+    assert torch.equal(pos.reshape(-1).long(), rank)
