@@ -28,8 +28,8 @@
 // MMA's own (tensor pipe 47-51 % active; 16384 x 4096 x 7168 without extras 463
 // us, 2.08 PFLOP/s). Its loop has to keep two loads of 32 columns in flight and
 // spill nothing: with one load 750 us, with 100 bytes of spills 670. Few rows:
-// the weights' stream from HBM (64 rows on 32 experts of 4096 x 7168: 141 us,
-// 5.8 TB/s, 0.89 of the copy rate).
+// the weights' stream from HBM (64 rows on 32 experts of 4096 x 7168: 145 us,
+// 5.6 TB/s, 0.86 of the copy rate; call after call, at the power limit, 163).
 #include "bq.h"
 #include "bq_device.cuh"
 #include "bq_epi.cuh"
@@ -44,16 +44,17 @@ constexpr int X_TABLE = 256;                 // entries of the tile table
 constexpr int REGX_LAUNCH = 168, REGX_CTL = 88, REGX_ACC = 208;
 static_assert(128 * REGX_CTL + 256 * REGX_ACC <= X_NT * REGX_LAUNCH, "register split");
 
-// XR: rows of a tile. The MMA always takes 128; with XR = 32 a slot holds 32 and
-// the rest of what it reads is other slots' bytes, which reach rows of the
-// result that nothing reads. That leaves the ring to the weights.
+// XR: rows of a tile. The MMA always takes 128; behind a tile of 32 a slot holds
+// zeros. Slots of 32 rows, with other slots' bytes behind them, leave the ring a
+// fourth stage, but products that nobody reads cost clock at the power limit (64
+// rows on 32 experts of 4096 x 7168, call after call: 173 us against 163).
 template <int BN, int XR>
 struct PlanX {
     // k-blocks of a ring stage and of a TMEM buffer: each signal between the
     // roles costs the single threads that issue loads and MMAs some 70 clocks, so
     // narrow tiles, whose k-blocks are short, share one between two.
     static constexpr int KS = BN == 256 ? 1 : 2;
-    static constexpr uint32_t A_BYTES = XR * XK, W_BYTES = BN * XK; // of a k-block
+    static constexpr uint32_t A_BYTES = XM * XK, W_BYTES = BN * XK; // of a k-block
     // Ring stages. The widest tiles give one up for a ring of scales.
     static constexpr bool SCALES = BN == 256;
     static constexpr int S = (int)((SCALES ? 147456 : 196608) / (KS * (A_BYTES + W_BYTES)));
@@ -71,7 +72,6 @@ struct PlanX {
     static constexpr uint32_t SMEM = OFF_TABLE + X_TABLE * 4 + 1024; // room to align the base to 1024
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static_assert(W_BYTES % 2048 == 0, "both weight boxes start on 1024-byte boundaries");
-    static_assert(S * KS * W_BYTES >= XM * XK, "the MMA's 128 rows from the last slot stay inside the ring");
     static_assert(TMEM == 512 || TMEM == 256, "a power of two");
 };
 // One lane of a converged warp.
@@ -246,6 +246,13 @@ __global__ void __launch_bounds__(X_NT, 1) k_fp8_experts(const __grid_constant__
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 8 && lane == 0) { prefetch_map(&tm_a); prefetch_map(&tm_w); }
+    if constexpr (XR < XM) {
+        // The tensor core multiplies the rows behind a tile's as well, and at the
+        // card's power limit that costs clock. Zeros cost least.
+        for (uint32_t i = threadIdx.x * 16u; i < S * KS * P::A_BYTES; i += X_NT * 16u)
+            *reinterpret_cast<uint4*>(sb + P::OFF_A + i) = make_uint4(0u, 0u, 0u, 0u);
+        fence_async_shared();
+    }
     if (warp == 9) tmem_alloc(base + P::OFF_MISC, P::TMEM);
     // Row tiles before each table entry (exclusive sums over warps 0-7).
     int mine = 0, incl = 0;
