@@ -10,6 +10,8 @@ torch tensors; no value is computed in Python.
 
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _bq as B
@@ -359,6 +361,16 @@ def fp8_tensor_dequantize(e, scale, ydtype=torch.bfloat16, stream=None):
 
 
 # ---------------------------------------------------------------- dense epilogue
+def _scratch_of(stream, like):
+    """Scratch allocated in this context belongs to the stream that uses it: once
+    the call drops it, nobody gets it before that stream's work is done."""
+    if stream is None or not like.is_cuda:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=like.device)
+    return torch.cuda.stream(stream)
+
+
 def fp8_block_gemm_epilogue(a_e4m3, a_scale, w_e4m3, w_scale, bias=None, act: str = "none", residual=None,
                             out_dtype=torch.bfloat16, save_pre: bool = False, stream=None):
     """act(A @ W^T + bias) + residual from quantized activations (as
@@ -383,7 +395,8 @@ def gemm_epilogue_backward(dy, pre, act: str, bias_grad: bool = True, stream=Non
     dbias = ws = None
     if bias_grad:
         dbias = torch.empty(n, dtype=torch.float32, device=dy.device)
-        ws = torch.empty(B.bq_gemm_epilogue_backward_workspace_size(m, n), dtype=torch.uint8, device=dy.device)
+        with _scratch_of(stream, dy):
+            ws = torch.empty(B.bq_gemm_epilogue_backward_workspace_size(m, n), dtype=torch.uint8, device=dy.device)
     B.bq_gemm_epilogue_backward(dy, pre, act, dz, dbias, ws, stream)
     return dz, dbias
 
@@ -472,10 +485,13 @@ def fp8_moe(x, logits, w1, w1_scale, w2, w2_scale, top_k: int, bias=None, score:
     out: with experts spread over GPUs their sums are added up) with 128x128
     scales. i % 128 == 0 and h % 128 == 0. Returns [t, h] in x's dtype."""
     with torch.cuda.device(x.device):
-        ids, w = moe_route(logits, top_k, bias, score, n_groups, top_groups, group_top, renormalize, scale, stream)
-        offsets, rows, pos = moe_group(ids, w1.shape[0], first_expert, stream)
-        ea, sa = fp8_block_quantize(x, 1, 128, stream=stream)
-        h = fp8_grouped_gemm(ea, sa, offsets, w1, w1_scale, rows, None, act, True, x.dtype, stream=stream)
-        eh, sh = fp8_block_quantize(h, 1, 128, stream=stream)
-        y = fp8_grouped_gemm(eh, sh, offsets, w2, w2_scale, out_dtype=x.dtype, stream=stream)
-        return moe_combine(y, pos, w, residual=residual, stream=stream)
+        out = torch.empty((x.shape[0], w2.shape[1]), dtype=x.dtype, device=x.device)
+        with _scratch_of(stream, x):                  # and every call below goes to that stream
+            ids, w = moe_route(logits, top_k, bias, score, n_groups, top_groups, group_top, renormalize, scale)
+            offsets, rows, pos = moe_group(ids, w1.shape[0], first_expert)
+            ea, sa = fp8_block_quantize(x, 1, 128)
+            h = fp8_grouped_gemm(ea, sa, offsets, w1, w1_scale, rows, None, act, True, x.dtype)
+            eh, sh = fp8_block_quantize(h, 1, 128)
+            y = fp8_grouped_gemm(eh, sh, offsets, w2, w2_scale, out_dtype=x.dtype)
+            B.bq_moe_combine(y, pos, w, residual, out)
+    return out

@@ -561,3 +561,31 @@ def test_epilogue_shared_tiles_odd_widths(bq, m, n, k):
     got, pre = bq.api.fp8_block_gemm_epilogue(a, sa, w, sw, bias, "silu", res, HF, True)
     bound_check(pre, z, d, HF, "pre")
     bound_check(got, v + res.double(), dv + 2.0 ** -24 * ((v + res.double()).abs() + dv), HF, f"{m}x{n}x{k}")
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_scratch_belongs_to_the_stream_that_uses_it(bq, raw):
+    """A call given another stream, which is busy: what the current stream allocates and writes after the call
+    returned is not the call's scratch."""
+    g = torch.Generator().manual_seed(30)
+    e, h = 8, 256
+    w1, s1 = codes((e, 512, h), g, 128)
+    w2, s2 = codes((e, h, 256), g, 128)
+    x = torch.randn((300, h), generator=g).bfloat16().cuda()
+    logits = torch.randn((300, e), generator=g).cuda()
+    dy, pre = (torch.randn((2000, 320), generator=g).bfloat16().cuda() for _ in range(2))
+    want = bq.api.fp8_moe(x, logits, w1, s1, w2, s2, 4)
+    want_dz, want_db = bq.api.gemm_epilogue_backward(dy, pre, "silu")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    arg = s.cuda_stream if raw else s
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)                # some 50 ms
+    out = bq.api.fp8_moe(x, logits, w1, s1, w2, s2, 4, stream=arg)
+    dz, db = bq.api.gemm_epilogue_backward(dy, pre, "silu", stream=arg)
+    held = [torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+            for n in (512, 4096, 8192, 70_000, 160_000, 400_000, 700_000, 1 << 20) for _ in range(20)]
+    torch.cuda.current_stream().synchronize()
+    s.synchronize()
+    assert torch.equal(out, want) and torch.equal(dz, want_dz) and torch.equal(db, want_db)
+    assert all(bool((t == 255).all()) for t in held)
