@@ -366,8 +366,8 @@ def _scratch_of(stream, like):
     the call drops it, nobody gets it before that stream's work is done."""
     if stream is None or not like.is_cuda:
         return contextlib.nullcontext()
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=like.device)
+    if isinstance(stream, int):                       # (a wrapper made for handle 0 would be a new stream)
+        stream = torch.cuda.ExternalStream(stream, device=like.device) if stream else torch.cuda.default_stream(like.device)
     return torch.cuda.stream(stream)
 
 

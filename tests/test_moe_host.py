@@ -125,3 +125,16 @@ def test_binding_checks_shapes_and_devices(B):
     with pytest.raises(ValueError, match="contiguous"):
         need(t.t(), "t", (6, 4), (torch.float32,), 0)
     assert need(None, "t", (1,), (torch.float32,), 0) is None
+
+
+def test_scratch_of_the_default_stream(B, monkeypatch):
+    """A stream given by its handle: 0 is the device's default stream (a wrapper around handle 0 would be another, new stream)."""
+    import types
+
+    import dequantize_absmax_reduce_b200 as bq
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: ("external", handle, device))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: ("default", device))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    like = types.SimpleNamespace(is_cuda=True, device="cuda:3")
+    assert bq.api._scratch_of(0, like) == ("default", "cuda:3")
+    assert bq.api._scratch_of(0x5500, like) == ("external", 0x5500, "cuda:3")
