@@ -26,10 +26,11 @@ constexpr unsigned FULL = 0xffffffffu;
 // sum of such terms, a reciprocal and a product, on values of at most 1; a sigmoid
 // has less) and the sum with the bias by 2^-24 of its size. Values nearer than
 // 2^-18 max(1, |v|) to one another, and what the keys' low bits take (sums of two:
-// 1.5 * 2^-17), are looked at again in f64: the candidates alone, those too near
-// the last to be told from it among them, or the groups' sums. That happens to
-// about one row in a hundred of 256 experts. In f64 throughout, 16384 such rows
-// took 65 us; with the near rows chosen anew in f64, their wait alone cost 7 us.
+// 1.5 * 2^-18 max(1, |v|) each, v the larger member), are looked at again in f64:
+// the candidates alone, those too near the last to be told from it among them, or
+// the groups' sums. That happens to about one row in a hundred of 256 experts. In
+// f64 throughout, 16384 such rows took 65 us; with the near rows chosen anew in
+// f64, their wait alone cost 7 us.
 //
 // A lane sorts its values once, as integers in their order whose lowest bits give
 // way to the value's number in the lane (the nearness test allows for that; so do
@@ -358,23 +359,29 @@ __global__ void __launch_bounds__(128, C <= 8 ? 7 : 2) k_moe_route(const RouteAr
             }
             bool kept = false, near = false;
             if (SCORED || a.group_top == 1) {
-                // Values fit f32 (sums of scores: nearly): the best top_groups one by
-                // one, and whether the next one is near the last.
-                float gv = g1 ? key_value(g1) : -CUDART_INF_F;
-                if (a.group_top == 2 && g2) gv += key_value(g2);
-                uint32_t gk = g1 ? order_key(gv + 0.0f) : 0u, last = 0u;
+                // Values fit f32 (sums of scores: nearly): the best top_groups one by one.
+                const bool two = a.group_top == 2 && g2 != 0u;
+                const float v1 = g1 ? key_value(g1) : -CUDART_INF_F, v2 = two ? key_value(g2) : 0.0f;
+                const float gv = v1 + v2;
+                uint32_t gk = g1 ? order_key(gv + 0.0f) : 0u;
                 for (int r = 0; r < a.top_groups; ++r) {
                     const uint32_t m = __reduce_max_sync(FULL, gk);
                     if (m == 0u) break;
-                    last = m;
                     const int w = __shfl_sync(FULL, mine, __ffs(__ballot_sync(FULL, gk == m)) - 1);
                     if (mine == w) { kept = true; gk = 0u; }
                 }
                 if (SCORED) {
-                    const uint32_t m = __reduce_max_sync(FULL, gk);
-                    const float v = key_value(last);
-                    // (written so that infinities count as near)
-                    near = m != 0u && !(v - key_value(m) > 0x1.8p-17f * fmaxf(1.0f, fabsf(v)) + C * 0x1p-22f * fabsf(v));
+                    // A sum is off by what its members are off, however small it is itself:
+                    // near where the lowest that a group that stays may lie is not above the
+                    // highest that one left out may. (A key's low bits are up to C steps of 2^-23
+                    // of the value; 96 * 2^-24 holds the scores' errors and the roundings.)
+                    const float size = fmaxf(fabsf(v1), fabsf(v2));
+                    const float err = 0x1.8p-18f * fmaxf(1.0f, size) + C * 0x1p-22f * size;
+                    const bool fin = fabsf(v1) + fabsf(v2) < CUDART_INF_F;   // (a packed infinity reads as NaN)
+                    const float lo = fin ? gv - err : -CUDART_INF_F, hi = fin ? gv + err : CUDART_INF_F;
+                    const uint32_t least_in = __reduce_min_sync(FULL, g1 && kept ? order_key(lo) : FULL);
+                    const uint32_t most_out = __reduce_max_sync(FULL, g1 && !kept ? order_key(hi) : 0u);
+                    near = most_out >= least_in;
                 }
             } else {
                 const int every = by_lane ? a.group_lanes : 1;

@@ -44,3 +44,33 @@ def test_stream_zero_is_the_default_stream(bq):
     out = bq.api.fp8_moe(x, logits, *weights, 4, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+# ---------------------------------------------------------------- choice of groups
+def chosen_in_64_bits(x, bias, score, ng, tg, top_k):
+    """Ids by f64 choice values score + bias, groups by the sum of their two largest; the lowest index of equal ones."""
+    x = x.double()
+    v = (torch.sigmoid(x) if score == "sigmoid" else torch.softmax(x, -1)) + bias.double()
+    groups = v.reshape(x.shape[0], ng, -1)
+    value = torch.sort(groups, dim=-1, descending=True).values[..., :2].sum(-1)
+    kept = torch.zeros_like(value, dtype=torch.bool)
+    kept.scatter_(1, torch.sort(value, dim=-1, descending=True, stable=True).indices[:, :tg], True)
+    v = torch.where(kept[..., None], groups, -math.inf).reshape(x.shape)
+    return torch.sort(v, dim=-1, descending=True, stable=True).indices[:, :top_k].to(torch.int32)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("e,ng,tg,k", [(256, 8, 4, 8), (64, 32, 16, 8), (60, 5, 2, 4), (512, 16, 3, 6)])
+@pytest.mark.parametrize("size", [10.0, 50.0, 1e3, 1e4])
+def test_group_sums_that_cancel(bq, score, e, ng, tg, k, size):
+    """A group's two best choice values of opposite sign, far larger than their sum: the groups that stay are those of f64
+    sums all the same (where groups end with lanes, and where they do not)."""
+    g = gen(e + ng + int(size))
+    x = torch.randn((3000, e), generator=g)
+    bias = torch.full((ng, e // ng), -3.0 * size)
+    bias[:, 0], bias[:, 1] = size, -size
+    bias = bias.reshape(-1) + 0.01 * torch.rand(e, generator=g)
+    ids, _ = bq.api.moe_route(x.cuda(), k, bias.cuda(), score, ng, tg, 2)
+    want = chosen_in_64_bits(x, bias, score, ng, tg, k)
+    wrong = (ids.cpu() != want).any(1)
+    assert not wrong.any(), f"{int(wrong.sum())} rows of 3000"
