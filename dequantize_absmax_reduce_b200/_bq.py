@@ -41,6 +41,7 @@ MODE = {"dynamic": BQ_SCALE_DYNAMIC, "static": BQ_SCALE_STATIC, "from_range": BQ
 ROUND = {"rne": BQ_RNE, "rhaz": BQ_RHAZ}
 ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 SCORE = {"softmax": 0, "sigmoid": 1}
+BQ_GROUP_SCORES = 16
 
 
 class bq_qdesc(C.Structure):

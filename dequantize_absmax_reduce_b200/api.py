@@ -403,19 +403,23 @@ def gemm_epilogue_backward(dy, pre, act: str, bias_grad: bool = True, stream=Non
 
 # ---------------------------------------------------------------- expert layers
 def moe_route(logits, top_k: int, bias=None, score: str = "softmax", n_groups: int = 1, top_groups: int = 1,
-              group_top: int = 2, renormalize: bool = True, scale: float = 1.0, stream=None):
+              group_top: int | None = None, renormalize: bool = True, scale: float = 1.0, stream=None):
     """Experts of each token: logits [t, e] (f32 / f16 / bf16) -> (ids int32
     [t, top_k] by falling choice value, weights f32 [t, top_k]). Scores are the
     row's softmax or each logit's sigmoid; `bias` (f32 [e], for the balance of
     the load) is added for the choice only. With n_groups > 1 the choice is
-    limited to the top_groups groups of consecutive experts whose group_top
-    (1 or 2) best choice values sum highest. Weights are scale * score, divided
-    by the chosen scores' sum with renormalize. Experts at -inf are never
-    chosen: missing ones have id -1 and weight 0."""
+    limited to the top_groups groups of consecutive experts whose two best
+    scores + bias sum highest (no bias is a bias of zeros). group_top = 1 or 2
+    names the number of choice values to sum instead: score + bias, or without
+    a bias the logits themselves, whose sums of two stand in another order than
+    the scores'. Weights are scale * score, divided by the chosen scores' sum
+    with renormalize. Experts at -inf are never chosen: missing ones have id -1
+    and weight 0."""
     t = logits.shape[0]
     ids = logits.new_empty((t, top_k), dtype=torch.int32)
     w = logits.new_empty((t, top_k), dtype=torch.float32)
-    B.bq_moe_route(logits, bias, score, n_groups, top_groups, group_top, top_k, renormalize, scale, ids, w, stream)
+    B.bq_moe_route(logits, bias, score, n_groups, top_groups, B.BQ_GROUP_SCORES if group_top is None else group_top, top_k,
+                   renormalize, scale, ids, w, stream)
     return ids, w
 
 
@@ -483,11 +487,13 @@ def fp8_moe(x, logits, w1, w1_scale, w2, w2_scale, top_k: int, bias=None, score:
     logits [t, experts]; w1 [e, 2 i, h] (the gate's rows first) and w2 [e, h, i]
     E4M3 codes of the e experts from first_expert (the others' share is left
     out: with experts spread over GPUs their sums are added up) with 128x128
-    scales. i % 128 == 0 and h % 128 == 0. Returns [t, h] in x's dtype."""
+    scales. i % 128 == 0 and h % 128 == 0. Groups go by the sum of their
+    group_top (1 or 2) best scores + bias. Returns [t, h] in x's dtype."""
     with torch.cuda.device(x.device):
         out = torch.empty((x.shape[0], w2.shape[1]), dtype=x.dtype, device=x.device)
         with _scratch_of(stream, x):                  # and every call below goes to that stream
-            ids, w = moe_route(logits, top_k, bias, score, n_groups, top_groups, group_top, renormalize, scale)
+            ids, w = moe_route(logits, top_k, bias, score, n_groups, top_groups, None if group_top == 2 else group_top,
+                               renormalize, scale)
             offsets, rows, pos = moe_group(ids, w1.shape[0], first_expert)
             ea, sa = fp8_block_quantize(x, 1, 128)
             h = fp8_grouped_gemm(ea, sa, offsets, w1, w1_scale, rows, None, act, True, x.dtype)

@@ -20,8 +20,8 @@ constexpr unsigned FULL = 0xffffffffu;
 // that the lowest lane with the largest value holds the lowest index of it.
 //
 // The order of the choice values decides which experts a token gets, and it is
-// the order of f64 arithmetic. Without a bias the values are the logits, which
-// 32 bits hold exactly. With one, scores in f32 are off by less than 28 * 2^-24
+// the order of f64 arithmetic. Where the values are the logits, 32 bits hold them
+// exactly. Where they are scores (and biases), scores in f32 are off by less than 28 * 2^-24
 // (softmax: an exponential within 2 ulp, its argument's rounding, ten levels of a
 // sum of such terms, a reciprocal and a product, on values of at most 1; a sigmoid
 // has less) and the sum with the bias by 2^-24 of its size. Values nearer than
@@ -42,6 +42,7 @@ struct RouteArgs {
     const float* bias;
     int64_t tokens;
     int experts, top_k, n_groups, top_groups, group_top, sigmoid, renorm, vec;
+    int scored;                // choice values: score + bias (0 without one); else the logits
     int group_lanes;           // lanes of a group, a power of two, or 0: groups do not end with lanes
     int sum_lanes;             // half the power of two that holds top_k
     float scale;
@@ -109,7 +110,7 @@ __device__ __forceinline__ void exact_values(const RouteArgs& a, const T* row, i
         x[i] = e < a.experts ? (double)ld1<T>(row + e) : -CUDART_INF;
         if (x[i] > top) top = x[i];
     }
-    if (a.bias && !a.sigmoid) {
+    if (a.scored && !a.sigmoid) {
         top = warp_max(top);
 #pragma unroll
         for (int i = 0; i < C; ++i) {
@@ -121,7 +122,7 @@ __device__ __forceinline__ void exact_values(const RouteArgs& a, const T* row, i
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         const int e = lane * C + i;
-        const double s = !a.bias ? x[i] : a.sigmoid ? 1.0 / (1.0 + exp(-x[i])) : v[i] / sum;
+        const double s = !a.scored ? x[i] : a.sigmoid ? 1.0 / (1.0 + exp(-x[i])) : v[i] / sum;
         v[i] = a.bias && e < a.experts ? s + (double)__ldg(a.bias + e) : s;
         if (!(x[i] > -CUDART_INF) || v[i] != v[i]) v[i] = -CUDART_INF;
     }
@@ -172,7 +173,7 @@ __device__ __noinline__ unsigned exact_groups(const RouteArgs& a, const T* row, 
 template <class T, int C>
 __device__ __noinline__ int exact_order(const RouteArgs& a, const T* row, int lane, int id, int n, double* room) {
     double v = -CUDART_INF;
-    if (a.bias && !a.sigmoid) {
+    if (a.scored && !a.sigmoid) {
         double all[C];
         exact_values<T, C>(a, row, lane, all);
         __syncwarp();
@@ -184,7 +185,7 @@ __device__ __noinline__ int exact_order(const RouteArgs& a, const T* row, int la
         __syncwarp();
     } else if (id >= 0) {
         const double x = (double)ld1<T>(row + id);
-        v = a.bias ? 1.0 / (1.0 + exp(-x)) + (double)__ldg(a.bias + id) : x;
+        v = a.scored ? 1.0 / (1.0 + exp(-x)) + (a.bias ? (double)__ldg(a.bias + id) : 0.0) : x;
     }
     int rank = 0;
     for (int j = 0; j < n; ++j) {
@@ -263,7 +264,7 @@ __device__ __forceinline__ bool too_near(uint32_t hi, uint32_t lo) {
     }
 }
 
-// SCORED: choice values are score + bias; else the logits.
+// SCORED: choice values are score + bias (0 without one); else the logits.
 // (Up to eight experts a lane seven CTAs share an SM: 26.0 us at 16384 x 256 in
 // groups with a bias, five 28.4, nine 27.7.)
 template <class T, int C, bool SCORED>
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(128, C <= 8 ? 7 : 2) k_moe_route(const RouteAr
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         const bool in = lane * C + i < a.experts;
-        bias[i] = SCORED && in ? __ldg(a.bias + lane * C + i) : 0.0f;
+        bias[i] = SCORED && in && a.bias ? __ldg(a.bias + lane * C + i) : 0.0f;
         serve |= in && bias[i] > -CUDART_INF_F ? 1u << i : 0u;
     }
     for (int64_t t = (int64_t)blockIdx.x * 4 + warp; t < a.tokens; t += (int64_t)gridDim.x * 4) {
@@ -615,13 +616,13 @@ struct RouteLaunch {
         a.group_lanes = gsize % C == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
         const size_t smem = 4 * sizeof(double) * (size_t)a.experts;
         // (by the shared memory of a full width: the cached count serves every call)
-        static int with_bias[64] = {0}, without[64] = {0};
+        static int scored[64] = {0}, plain[64] = {0};
         unsigned grid = 0;
         const size_t most = 4 * sizeof(double) * 32 * C;
-        const cudaError_t e = a.bias ? resident_ctas(k_moe_route<T, C, true>, most, with_bias, a.tokens, &grid)
-                                     : resident_ctas(k_moe_route<T, C, false>, most, without, a.tokens, &grid);
+        const cudaError_t e = a.scored ? resident_ctas(k_moe_route<T, C, true>, most, scored, a.tokens, &grid)
+                                       : resident_ctas(k_moe_route<T, C, false>, most, plain, a.tokens, &grid);
         if (e != cudaSuccess) return e;
-        if (a.bias) k_moe_route<T, C, true><<<grid, 128, smem, st>>>(a);
+        if (a.scored) k_moe_route<T, C, true><<<grid, 128, smem, st>>>(a);
         else k_moe_route<T, C, false><<<grid, 128, smem, st>>>(a);
         return cudaGetLastError();
     }
@@ -1066,6 +1067,8 @@ extern "C" bq_status bq_moe_route(const void* logits, bq_dtype dtype, int64_t to
     if (tokens < 0 || experts < 1 || experts > 1024 || top_k < 1 || top_k > 32) return BQ_ERR_INVALID_ARG;
     if (n_groups < 1 || n_groups > 32 || experts % n_groups != 0 || top_groups < 1 || top_groups > n_groups)
         return BQ_ERR_INVALID_ARG;
+    const bool by_score = group_top == BQ_GROUP_SCORES;
+    if (by_score) group_top = BQ_GROUP_TWO_BEST;
     if (group_top < 1 || group_top > 2 || top_k > top_groups * (experts / n_groups)) return BQ_ERR_INVALID_ARG;
     if (!pairs_fit(tokens, top_k)) return BQ_ERR_INVALID_ARG;
     if (tokens == 0) return BQ_OK;
@@ -1073,7 +1076,7 @@ extern "C" bq_status bq_moe_route(const void* logits, bq_dtype dtype, int64_t to
     if (misaligned(logits, type_mask(dtype)) || misaligned(bias, 3) || misaligned(ids, 3) || misaligned(weights, 3))
         return BQ_ERR_MISALIGNED;
     RouteArgs a{logits, bias, tokens, experts, top_k, n_groups, top_groups, group_top, score == BQ_SCORE_SIGMOID,
-                renormalize != 0, 0, 0, 0, scale, ids, weights};
+                renormalize != 0, 0, bias || (by_score && n_groups > 1), 0, 0, scale, ids, weights};
     while (2 * a.sum_lanes < top_k) a.sum_lanes = a.sum_lanes ? 2 * a.sum_lanes : 1;
     cudaStream_t st = (cudaStream_t)stream;
     if (dtype == BQ_F32) return from(by_width<float, RouteLaunch>(a, st));

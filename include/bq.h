@@ -605,6 +605,7 @@ bq_status bq_gemm_epilogue_backward(const void* dy, const void* pre, bq_dtype dt
  * pairs in expert order, bq_fp8_grouped_gemm multiplies every expert's rows by
  * its weights, bq_moe_combine sums the experts' rows back into tokens. */
 typedef enum bq_score { BQ_SCORE_SOFTMAX = 0, BQ_SCORE_SIGMOID = 1 } bq_score;
+typedef enum bq_group_top { BQ_GROUP_BEST = 1, BQ_GROUP_TWO_BEST = 2, BQ_GROUP_SCORES = 16 } bq_group_top;
 
 /* Choice of experts. logits [tokens, experts] F32, F16 or BF16. The score s of
  * an expert is its logit's softmax over the row or its sigmoid; its choice
@@ -614,7 +615,10 @@ typedef enum bq_score { BQ_SCORE_SOFTMAX = 0, BQ_SCORE_SIGMOID = 1 } bq_score;
  * of -inf or NaN, or a choice value of -inf or NaN, is not available.
  * Experts form n_groups groups of equal size, consecutive; a group's value is
  * the sum of its group_top (1 or 2) largest available choice values (-inf with
- * none). The top_groups groups of largest value stay, and of their experts the
+ * none). Logits and scores have the same order, but sums of two of them do not:
+ * routers sum scores, so without a bias pass BQ_GROUP_SCORES, which with several
+ * groups makes every choice value s + bias (0 without one) and sums the two
+ * largest: the ids and weights that a bias of zeros gives. The top_groups groups of largest value stay, and of their experts the
  * top_k of largest choice value are chosen; of equal values the lowest index
  * goes first, for groups and experts alike.
  *   ids     int32 [tokens, top_k], by falling choice value; -1 where fewer

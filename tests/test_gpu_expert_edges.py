@@ -74,3 +74,36 @@ def test_group_sums_that_cancel(bq, score, e, ng, tg, k, size):
     want = chosen_in_64_bits(x, bias, score, ng, tg, k)
     wrong = (ids.cpu() != want).any(1)
     assert not wrong.any(), f"{int(wrong.sum())} rows of 3000"
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("dtype", [F32, BF, HF])
+@pytest.mark.parametrize("e,ng,tg,k", [(256, 8, 4, 8), (64, 8, 3, 4), (60, 5, 2, 4), (1024, 32, 7, 32), (8, 4, 2, 2)])
+def test_groups_without_a_bias_are_those_of_zero_biases(bq, score, dtype, e, ng, tg, k):
+    """Groups go by sums of scores, whether a bias of zeros is given or none."""
+    x = (1.5 * torch.randn((500, e), generator=gen(e + k))).to(dtype)
+    x[3, : e // 2] = -math.inf
+    x[4] = -math.inf
+    x[5, 1:] = -math.inf
+    x[6] = 0.5
+    zeros = torch.zeros(e)
+    for renorm in (True, False):
+        ids, w = bq.api.moe_route(x.cuda(), k, score=score, n_groups=ng, top_groups=tg, renormalize=renorm)
+        ids0, w0 = bq.api.moe_route(x.cuda(), k, zeros.cuda(), score, ng, tg, 2, renorm)
+        assert torch.equal(ids, ids0) and torch.equal(w, w0)
+    full = torch.isfinite(x.double()).all(1)
+    assert torch.equal(ids.cpu()[full], chosen_in_64_bits(x[full], zeros, score, ng, tg, k))
+
+
+def test_layer_without_a_bias_is_that_of_zero_biases(bq):
+    g = gen(31)
+    e, h = 16, 256
+    x = torch.randn((200, h), generator=g).bfloat16().cuda()
+    logits = (1.5 * torch.randn((200, e), generator=g)).cuda()
+    w1, s1 = bq.api.fp8_block_quantize((0.05 * torch.randn((e * 512, h), generator=g)).bfloat16().cuda(), 128)
+    w2, s2 = bq.api.fp8_block_quantize((0.05 * torch.randn((e * h, 256), generator=g)).bfloat16().cuda(), 128)
+    weights = (w1.view(e, 512, h), s1.view(e, 4, 2), w2.view(e, h, 256), s2.view(e, 2, 2))
+    for top in ({}, {"group_top": 1}, {"group_top": 2}):
+        kw = {"score": "sigmoid", "n_groups": 4, "top_groups": 2, **top}
+        assert torch.equal(bq.api.fp8_moe(x, logits, *weights, 4, **kw),
+                           bq.api.fp8_moe(x, logits, *weights, 4, bias=torch.zeros(e, device="cuda"), **kw))

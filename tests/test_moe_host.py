@@ -138,3 +138,11 @@ def test_scratch_of_the_default_stream(B, monkeypatch):
     like = types.SimpleNamespace(is_cuda=True, device="cuda:3")
     assert bq.api._scratch_of(0, like) == ("default", "cuda:3")
     assert bq.api._scratch_of(0x5500, like) == ("external", 0x5500, "cuda:3")
+
+
+def test_route_group_values(B):
+    """BQ_GROUP_SCORES is a third way to value groups; numbers between are none."""
+    assert _route(B, t=0, gt=B.BQ_GROUP_SCORES) == B.BQ_OK
+    for gt in (B.BQ_GROUP_SCORES - 1, B.BQ_GROUP_SCORES + 1, -1):
+        assert _route(B, t=0, gt=gt) == B.BQ_ERR_INVALID_ARG
+    assert _route(B, gt=B.BQ_GROUP_SCORES, k=33) == B.BQ_ERR_INVALID_ARG
