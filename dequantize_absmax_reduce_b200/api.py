@@ -447,8 +447,8 @@ def moe_group(ids, n_experts: int, first_expert: int = 0, stream=None):
 
 def moe_combine(y, pos, weights, residual=None, out_dtype=None, stream=None):
     """out[t] = residual[t] + sum_j weights[t, j] * y[pos[t, j]] (a position
-    outside y adds nothing), in out_dtype (y's unless given; a residual has it
-    too)."""
+    outside y adds nothing; a NaN weight makes the token NaN all the same), in
+    out_dtype (y's unless given; a residual has it too)."""
     out = torch.empty((pos.shape[0], y.shape[1]), dtype=out_dtype or y.dtype, device=y.device)
     B.bq_moe_combine(y, pos, weights, residual, out, stream)
     return out

@@ -832,7 +832,7 @@ cudaError_t launch_group(GroupArgs a, cudaStream_t st) {
 
 // ---------------------------------------------------------------- combine
 // out[t] = residual[t] + sum over slots of weights[t, j] * y[pos[t, j]], in f32
-// and rounded once. One pass over memory: a thread owns one 16-byte vector of
+// and rounded once; NaN where a weight is. One pass over memory: a thread owns one 16-byte vector of
 // out and loads that vector of every slot's row before it adds them up.
 struct CombineArgs {
     const void* y;
@@ -859,12 +859,16 @@ __global__ void __launch_bounds__(128) k_moe_combine(const CombineArgs a) {
         const float* weights = a.weights + t * a.top_k;
         int p[B];
         float w[B];
+        // NaN weights mark a row of NaN logits, which may have no expert, here or
+        // anywhere: its token becomes NaN with or without a row to add.
+        bool bad = false;
         auto slots = [&](int j0) {
 #pragma unroll
             for (int j = 0; j < B; ++j) {
                 p[j] = j0 + j < a.top_k ? __ldg(pos + j0 + j) : -1;
                 w[j] = j0 + j < a.top_k ? __ldg(weights + j0 + j) : 0.0f;
                 if (p[j] >= a.y_rows) p[j] = -1;
+                bad |= w[j] != w[j];
             }
         };
         slots(0);
@@ -906,6 +910,10 @@ __global__ void __launch_bounds__(128) k_moe_combine(const CombineArgs a) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (c0 + u * run >= a.hidden) break;
+                if (bad) {
+#pragma unroll
+                    for (int i = 0; i < W; ++i) acc[u][i] = CUDART_NAN_F;
+                }
                 if (res) {
                     float x[W];
                     r[u].get(x);

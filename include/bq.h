@@ -625,7 +625,8 @@ typedef enum bq_group_top { BQ_GROUP_BEST = 1, BQ_GROUP_TWO_BEST = 2, BQ_GROUP_S
  *           experts are available;
  *   weights f32 [tokens, top_k] = scale * s / D with D the sum of the chosen
  *           experts' scores (renormalize) or 1; 0 where the id is -1. A row
- *           with a NaN logit gets NaN weights, so that it does not go unseen.
+ *           with a NaN logit gets NaN weights, also where the id is -1, and
+ *           bq_moe_combine passes them on, so that it does not go unseen.
  * A softmax row whose largest logit is +inf gives those experts equal shares.
  * experts <= 1024, n_groups <= 32 dividing experts, top_k <= 32 and <=
  * top_groups * experts / n_groups; tokens * top_k < 2^31. */
@@ -659,7 +660,8 @@ bq_status bq_moe_group(const int32_t* ids, int64_t tokens, int32_t top_k, int32_
 
 /* out[t] = residual[t] + sum over slots j of weights[t, j] * y[pos[t, j]], in
  * f32 in the order of the slots, the residual last, rounded once. y [y_rows,
- * hidden] (y_dtype F32, F16 or BF16); a pos outside [0, y_rows) adds nothing;
+ * hidden] (y_dtype F32, F16 or BF16); a pos outside [0, y_rows) adds nothing,
+ * but a NaN among a token's weights makes its out NaN whatever its positions;
  * residual [tokens, hidden] of out's dtype, NULL for none; it may be out. */
 bq_status bq_moe_combine(const void* y, bq_dtype y_dtype, int64_t y_rows, int64_t hidden,
                          const int32_t* pos, const float* weights, int64_t tokens, int32_t top_k,

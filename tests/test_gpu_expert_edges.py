@@ -107,3 +107,41 @@ def test_layer_without_a_bias_is_that_of_zero_biases(bq):
         kw = {"score": "sigmoid", "n_groups": 4, "top_groups": 2, **top}
         assert torch.equal(bq.api.fp8_moe(x, logits, *weights, 4, **kw),
                            bq.api.fp8_moe(x, logits, *weights, 4, bias=torch.zeros(e, device="cuda"), **kw))
+
+
+# ---------------------------------------------------------------- NaN logits
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("k", [1, 4, 8, 9, 40])
+@pytest.mark.parametrize("h", [64, 7])
+def test_nan_weight_without_a_row_is_seen(bq, dtype, k, h):
+    """A NaN weight, which marks a row of NaN logits, makes its token NaN although the position names no row."""
+    y = torch.ones((50, h), dtype=dtype, device="cuda")
+    pos = torch.full((6, k), -1, dtype=torch.int32)
+    w = torch.full((6, k), 0.25)
+    pos[0], pos[1] = 3, 3
+    w[1, -1] = math.nan
+    w[2] = math.nan
+    w[3, -1], pos[3, -1] = math.nan, 50
+    w[4, 0] = math.inf                              # not a NaN: nothing to add, nothing added
+    res = torch.ones((6, h), dtype=dtype, device="cuda")
+    for r in (None, res):
+        out = bq.api.moe_combine(y, pos.cuda(), w.cuda(), r).float().cpu()
+        assert (out[0] == 0.25 * k + (r is not None)).all() and torch.isnan(out[1:4]).all()
+        assert (out[4:] == (0 if r is None else 1)).all()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_layer_shows_a_token_of_nan_logits(bq, score):
+    """One NaN logit or nothing but NaN: the token comes out as NaN on every GPU that holds some of the experts, padded
+    tokens (-inf) as their residual."""
+    g = gen(81)
+    x = torch.randn((6, 256), generator=g).bfloat16().cuda()
+    w1, s1 = bq.api.fp8_block_quantize((0.05 * torch.randn((8 * 512, 256), generator=g)).bfloat16().cuda(), 128)
+    w2, s2 = bq.api.fp8_block_quantize((0.05 * torch.randn((8 * 256, 256), generator=g)).bfloat16().cuda(), 128)
+    w1, s1, w2, s2 = w1.view(8, 512, 256), s1.view(8, 4, 2), w2.view(8, 256, 256), s2.view(8, 2, 2)
+    logits = torch.randn((6, 8), generator=g)
+    logits[1], logits[2], logits[4, 3] = math.nan, -math.inf, math.nan
+    res = torch.randn((6, 256), generator=g).bfloat16().cuda()
+    for a, b in ((0, 8), (0, 4), (4, 8)):
+        out = bq.api.fp8_moe(x, logits.cuda(), w1[a:b], s1[a:b], w2[a:b], s2[a:b], 3, score=score, first_expert=a, residual=res)
+        assert torch.isnan(out[[1, 4]]).all() and torch.equal(out[2], res[2]) and torch.isfinite(out[[0, 2, 3, 5]]).all()
