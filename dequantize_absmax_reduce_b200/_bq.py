@@ -115,6 +115,7 @@ _SIGS = {
     "bq_moe_group": [_P, _I64, _I32, _I32, _I32, _P, _P, _P, _P],
     "bq_moe_combine": [_P, C.c_int, _I64, _I64, _P, _P, _I64, _I32, _P, _P, C.c_int, _P],
     "bq_moe_combine_backward": [_P, _P, C.c_int, _I64, _I64, _P, _P, _I64, _I32, _P, _P, _P],
+    "bq_moe_combine_backward_whole": [_P, _P, C.c_int, _I64, _I64, _P, _P, _I64, _I32, _P, _P, _P, _SZ, _P],
     "bq_fp8_grouped_gemm": [_P, _P, _I64, _I64, _P, _P, _I32, _I64, _P, _P, _I64, _P, C.c_int, C.c_int, _I32, _P,
                             C.c_int, _P],
 }
@@ -134,6 +135,8 @@ lib.bq_packed_transpose_stride.argtypes = [_I64, _I64]
 lib.bq_packed_transpose_stride.restype = _I64
 lib.bq_gemm_epilogue_backward_workspace_size.argtypes = [_I64, _I64]
 lib.bq_gemm_epilogue_backward_workspace_size.restype = _SZ
+lib.bq_moe_combine_backward_workspace_size.argtypes = [_I64]
+lib.bq_moe_combine_backward_workspace_size.restype = _SZ
 lib.bq_check_device_error.argtypes = []
 lib.bq_check_device_error.restype = C.c_int
 
@@ -615,14 +618,27 @@ def bq_moe_combine(y, pos, weights, residual, out, stream=None):
           _need(residual, "residual", (t, h), (out.dtype,), dev), _need(out, "out", (t, h), _F, dev), DTYPE[out.dtype])
 
 
-def bq_moe_combine_backward(dout, y, pos, weights, dy, dweights, stream=None):
+def _combine_backward(fn, dout, y, pos, weights, dy, dweights, stream, *ws):
     p, h = y.shape
     t, top_k = pos.shape
     dev, dt = y.get_device(), (y.dtype,)
-    _call("bq_moe_combine_backward", dev, stream, _need(dout, "dout", (t, h), dt, dev), _need(y, "y", (p, h), _F, dev),
+    _call(fn, dev, stream, _need(dout, "dout", (t, h), dt, dev), _need(y, "y", (p, h), _F, dev),
           DTYPE[y.dtype], p, h, _need(pos, "pos", (t, top_k), _I32T, dev),
           _need(weights, "weights", (t, top_k), _F32, dev), t, top_k, _need(dy, "dy", (p, h), dt, dev),
-          _need(dweights, "dweights", (t, top_k), _F32, dev))
+          _need(dweights, "dweights", (t, top_k), _F32, dev), *ws)
+
+
+def bq_moe_combine_backward(dout, y, pos, weights, dy, dweights, stream=None):
+    _combine_backward("bq_moe_combine_backward", dout, y, pos, weights, dy, dweights, stream)
+
+
+def bq_moe_combine_backward_workspace_size(y_rows: int) -> int:
+    return int(lib.bq_moe_combine_backward_workspace_size(y_rows))
+
+
+def bq_moe_combine_backward_whole(dout, y, pos, weights, dy, dweights, ws, stream=None):
+    ws_at = _need(ws, "ws", (0 if ws is None else ws.numel(),), _U8T, y.get_device())
+    _combine_backward("bq_moe_combine_backward_whole", dout, y, pos, weights, dy, dweights, stream, ws_at, _nbytes(ws))
 
 
 def bq_fp8_grouped_gemm(a_e4m3, a_scale, rows, offsets, w_e4m3, w_scale, c, bias=None, act="none", gated=False,

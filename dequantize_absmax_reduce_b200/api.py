@@ -456,10 +456,12 @@ def moe_combine(y, pos, weights, residual=None, out_dtype=None, stream=None):
 
 def moe_combine_backward(dout, y, pos, weights, stream=None):
     """(dy like y, dweights f32 like weights) of moe_combine. Rows of dy that no
-    position names are not written."""
+    position names are zeros."""
     dy = torch.empty_like(y)
     dw = torch.empty_like(weights)
-    B.bq_moe_combine_backward(dout, y, pos, weights, dy, dw, stream)
+    with _scratch_of(stream, y):
+        ws = torch.empty(B.bq_moe_combine_backward_workspace_size(y.shape[0]), dtype=torch.uint8, device=y.device)
+    B.bq_moe_combine_backward_whole(dout, y, pos, weights, dy, dw, ws, stream)
     return dy, dw
 
 

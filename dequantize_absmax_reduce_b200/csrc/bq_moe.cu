@@ -935,6 +935,7 @@ struct CombineBwdArgs {
     const float* weights;
     void* dy;
     float* dweights;
+    int32_t* pair_of;          // [y_rows] or null: the pair (token, slot) that names each row, for k_zero_unnamed
     int64_t tokens, y_rows, hidden;
     int top_k;
 };
@@ -1003,9 +1004,44 @@ __global__ void __launch_bounds__(128) k_moe_combine_bwd(const CombineBwdArgs a)
         if (threadIdx.x < a.top_k) {
             float s = 0.0f;
             for (int w = 0; w < 4; ++w) s += part[threadIdx.x][w];
-            a.dweights[t * a.top_k + threadIdx.x] = s;
+            const int64_t pair = t * a.top_k + threadIdx.x;
+            a.dweights[pair] = s;
+            if (a.pair_of) {
+                const int p = a.pos[pair];
+                if (p >= 0 && p < a.y_rows) a.pair_of[p] = (int32_t)pair;
+            }
         }
         __syncthreads();
+    }
+    pdl_trigger();
+}
+
+// Zeros in the rows of dy that no position names. pair_of is not set up before:
+// where a row is not named it holds anything, but then the pair it tells of, if
+// there is one, has another position. Bound by the rows it writes (30720 of 32768
+// x 7168 bf16: 73 us, 6.0 TB/s); with every row named it reads 8 bytes a row, and
+// since it starts early costs 1.7 us beside the kernel before it (2049 x 6 x 4096
+// bf16: 39.4 -> 41.1; zeros in all of dy beforehand would write it twice). A warp
+// takes 8 rows.
+__global__ void __launch_bounds__(128) k_zero_unnamed(const int32_t* pair_of, const int32_t* pos, int pairs, int64_t rows,
+                                                      int64_t row_bytes, int wide, uint8_t* dy) {
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    for (int64_t r0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 5)) * 8; r0 < rows; r0 += (int64_t)gridDim.x * 32) {
+        const int64_t r = r0 + lane;
+        bool bare = false;
+        if (lane < 8 && r < rows) {
+            const int32_t pair = pairs > 0 ? pair_of[r] : -1;
+            bare = pair < 0 || pair >= pairs || pos[pair] != r;
+        }
+        for (unsigned todo = __ballot_sync(FULL, bare); todo; todo &= todo - 1) {
+            uint8_t* row = dy + (r0 + __ffs(todo) - 1) * row_bytes;
+            if (wide) {
+                for (int64_t i = lane * 16; i < row_bytes; i += 512) st16(row + i, U4{0u, 0u, 0u, 0u});
+            } else {
+                for (int64_t i = lane * 2; i < row_bytes; i += 64) *reinterpret_cast<uint16_t*>(row + i) = 0;
+            }
+        }
     }
 }
 
@@ -1051,6 +1087,16 @@ cudaError_t launch_combine_bwd(const CombineBwdArgs& a, cudaStream_t st) {
         case 2: k_moe_combine_bwd<T, 2, 4><<<grid, 128, 0, st>>>(a); break;
         default: k_moe_combine_bwd<T, 1, 4><<<grid, 128, 0, st>>>(a); break;
     }
+    return cudaGetLastError();
+}
+cudaError_t launch_zero_unnamed(const CombineBwdArgs& a, size_t es, cudaStream_t st) {
+    const int64_t row_bytes = a.hidden * (int64_t)es, need = (a.y_rows + 31) / 32, most = 16ll * sm_count();
+    const int wide = row_bytes % 16 == 0 && ((uintptr_t)a.dy & 15u) == 0, pairs = (int)(a.tokens * a.top_k);
+    const unsigned grid = (unsigned)(need < most ? need : most);
+    if (pairs > 0)
+        return launch_pdl(k_zero_unnamed, grid, 128, 0, st, (const int32_t*)a.pair_of, a.pos, pairs, a.y_rows, row_bytes, wide,
+                          (uint8_t*)a.dy);
+    k_zero_unnamed<<<grid, 128, 0, st>>>(a.pair_of, a.pos, pairs, a.y_rows, row_bytes, wide, (uint8_t*)a.dy);
     return cudaGetLastError();
 }
 
@@ -1139,23 +1185,48 @@ extern "C" bq_status bq_moe_combine(const void* y, bq_dtype y_dtype, int64_t y_r
     return from(combine_out<__nv_bfloat16>(a, out_dtype, st));
 }
 
-extern "C" bq_status bq_moe_combine_backward(const void* dout, const void* y, bq_dtype dtype, int64_t y_rows,
-                                             int64_t hidden, const int32_t* pos, const float* weights, int64_t tokens,
-                                             int32_t top_k, void* dy, float* dweights, void* stream) {
+static bq_status combine_backward(const void* dout, const void* y, bq_dtype dtype, int64_t y_rows, int64_t hidden,
+                                  const int32_t* pos, const float* weights, int64_t tokens, int32_t top_k, void* dy,
+                                  float* dweights, bool whole, void* ws, size_t ws_bytes, void* stream) {
     if (!float_type(dtype)) return BQ_ERR_UNSUPPORTED;
     if (y_rows < 0 || hidden < 0 || hidden >= (1ll << 31) || tokens < 0 || top_k < 1 || top_k > 32 ||
         !pairs_fit(tokens, top_k))
         return BQ_ERR_INVALID_ARG;
-    if (tokens == 0) return BQ_OK;
-    if ((!dout && hidden > 0) || ((!y || !dy) && y_rows > 0 && hidden > 0) || !pos || !weights || !dweights)
+    const bool zeros = whole && y_rows > 0 && hidden > 0;
+    if (whole && y_rows >= (1ll << 31)) return BQ_ERR_INVALID_ARG;
+    if (tokens == 0 && !zeros) return BQ_OK;
+    if (tokens > 0 && ((!dout && hidden > 0) || (!y && y_rows > 0 && hidden > 0) || !pos || !weights || !dweights))
         return BQ_ERR_INVALID_ARG;
+    if (!dy && y_rows > 0 && hidden > 0) return BQ_ERR_INVALID_ARG;
+    if (zeros && tokens > 0 && (!ws || ws_bytes < bq_moe_combine_backward_workspace_size(y_rows))) return BQ_ERR_INVALID_ARG;
     const uintptr_t m = type_mask(dtype);
     if (misaligned(dout, m) || misaligned(y, m) || misaligned(dy, m) || misaligned(pos, 3) || misaligned(weights, 3) ||
-        misaligned(dweights, 3))
+        misaligned(dweights, 3) || misaligned(ws, 3))
         return BQ_ERR_MISALIGNED;
-    CombineBwdArgs a{dout, y, pos, weights, dy, dweights, tokens, y_rows, hidden, top_k};
+    CombineBwdArgs a{dout, y, pos, weights, dy, dweights, zeros ? (int32_t*)ws : nullptr, tokens, y_rows, hidden, top_k};
     cudaStream_t st = (cudaStream_t)stream;
-    if (dtype == BQ_F32) return from(launch_combine_bwd<float>(a, st));
-    if (dtype == BQ_F16) return from(launch_combine_bwd<__half>(a, st));
-    return from(launch_combine_bwd<__nv_bfloat16>(a, st));
+    cudaError_t e = cudaSuccess;
+    if (tokens > 0)
+        e = dtype == BQ_F32 ? launch_combine_bwd<float>(a, st)
+            : dtype == BQ_F16 ? launch_combine_bwd<__half>(a, st)
+                              : launch_combine_bwd<__nv_bfloat16>(a, st);
+    if (e == cudaSuccess && zeros) e = launch_zero_unnamed(a, dtype == BQ_F32 ? 4 : 2, st);
+    return from(e);
+}
+
+extern "C" bq_status bq_moe_combine_backward(const void* dout, const void* y, bq_dtype dtype, int64_t y_rows,
+                                             int64_t hidden, const int32_t* pos, const float* weights, int64_t tokens,
+                                             int32_t top_k, void* dy, float* dweights, void* stream) {
+    return combine_backward(dout, y, dtype, y_rows, hidden, pos, weights, tokens, top_k, dy, dweights, false, nullptr, 0, stream);
+}
+
+extern "C" size_t bq_moe_combine_backward_workspace_size(int64_t y_rows) {
+    return y_rows > 0 && y_rows < (1ll << 31) ? (size_t)y_rows * sizeof(int32_t) : 0;
+}
+
+extern "C" bq_status bq_moe_combine_backward_whole(const void* dout, const void* y, bq_dtype dtype, int64_t y_rows,
+                                                   int64_t hidden, const int32_t* pos, const float* weights, int64_t tokens,
+                                                   int32_t top_k, void* dy, float* dweights, void* ws, size_t ws_bytes,
+                                                   void* stream) {
+    return combine_backward(dout, y, dtype, y_rows, hidden, pos, weights, tokens, top_k, dy, dweights, true, ws, ws_bytes, stream);
 }

@@ -675,6 +675,14 @@ bq_status bq_moe_combine_backward(const void* dout, const void* y, bq_dtype dtyp
                                   int64_t hidden, const int32_t* pos, const float* weights,
                                   int64_t tokens, int32_t top_k, void* dy, float* dweights,
                                   void* stream);
+/* The same with zeros in the rows of dy that no pos names (two launches). ws:
+ * scratch of bq_moe_combine_backward_workspace_size(y_rows) bytes (device,
+ * 4-byte aligned; its contents do not matter), y_rows < 2^31. */
+size_t bq_moe_combine_backward_workspace_size(int64_t y_rows);
+bq_status bq_moe_combine_backward_whole(const void* dout, const void* y, bq_dtype dtype, int64_t y_rows,
+                                        int64_t hidden, const int32_t* pos, const float* weights,
+                                        int64_t tokens, int32_t top_k, void* dy, float* dweights,
+                                        void* ws, size_t ws_bytes, void* stream);
 
 /* The experts' products in the block-FP8 format of bq_fp8_block_gemm_quantized.
  * For every expert e and every position p in [offsets[e], offsets[e + 1]):

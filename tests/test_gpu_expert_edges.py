@@ -145,3 +145,71 @@ def test_layer_shows_a_token_of_nan_logits(bq, score):
     for a, b in ((0, 8), (0, 4), (4, 8)):
         out = bq.api.fp8_moe(x, logits.cuda(), w1[a:b], s1[a:b], w2[a:b], s2[a:b], 3, score=score, first_expert=a, residual=res)
         assert torch.isnan(out[[1, 4]]).all() and torch.equal(out[2], res[2]) and torch.isfinite(out[[0, 2, 3, 5]]).all()
+
+
+def half_step(t, dtype):
+    fi = torch.finfo(dtype)
+    return t.abs() * (fi.eps / 2) + fi.smallest_normal * fi.eps / 2
+
+
+# ---------------------------------------------------------------- gradient rows that nobody names
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("t,k,h,p", [(1, 1, 1, 5), (5, 3, 7, 40), (33, 6, 1000, 500), (64, 8, 4096, 700), (9, 32, 136, 288), (0, 4, 64, 37),
+                                     (6, 2, 9001, 100), (20, 2, 66, 3000)])
+@pytest.mark.parametrize("stream", [None, "other", "raw"])
+def test_combine_backward_returns_no_unwritten_row(bq, dtype, t, k, h, p, stream):
+    """Rows of the returned gradient that no position names are zeros: memory that held NaN before is handed out."""
+    g = gen(t + k + h)
+    pos = torch.randperm(p, generator=g)[:t * k].reshape(t, k).to(torch.int32)
+    if t > 2:
+        pos[1], pos[2, 0], pos[2, -1] = -1, p, 2 ** 31 - 1
+    y = torch.randn((p, h), generator=g).to(dtype).cuda()
+    w = torch.rand((t, k), generator=g)
+    dout = torch.randn((t, h), generator=g).to(dtype)
+    s = None if stream is None else torch.cuda.Stream()
+    args = [v.cuda() for v in (dout, pos, w)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        held = [torch.full((p, h), math.nan, dtype=dtype, device="cuda"), torch.full((p,), 0, dtype=torch.int32, device="cuda")]
+        torch.cuda.synchronize()
+        del held
+        dy, dw = bq.api.moe_combine_backward(args[0], y, args[1], args[2], stream=s.cuda_stream if stream == "raw" else s)
+        torch.cuda.synchronize()
+        there = (pos >= 0) & (pos < p)
+        named = torch.zeros(p, dtype=torch.bool)
+        named[pos[there].long()] = True
+        assert (dy.cpu()[~named] == 0).all()
+        ref = torch.zeros((p, h), dtype=torch.float64)
+        ref[pos[there].long()] = (w.double()[..., None] * dout.double()[:, None, :])[there]
+        assert ((dy.cpu().double() - ref).abs() <= U * ref.abs() + half_step(ref * (1 + 2 * U), dtype)).all()
+        assert dw.shape == w.shape and (dw.cpu()[~there] == 0).all()
+
+
+def test_combine_backward_of_some_experts_in_a_graph(bq):
+    """Positions of a quarter of the experts, as the order gives them; captured once, replayed on another choice."""
+    g = gen(41)
+    t, k, h, e = 300, 4, 264, 32
+    ids = torch.stack([torch.randperm(e, generator=g)[:k] for _ in range(t)]).to(torch.int32).cuda()
+    y, dout = torch.randn((t * k, h), generator=g).bfloat16().cuda(), torch.randn((t, h), generator=g).bfloat16().cuda()
+    w = torch.rand((t, k), generator=g).cuda()
+
+    def step():
+        _, rows, pos = bq.api.moe_group(ids, 8, 8)
+        return rows, pos, *bq.api.moe_combine_backward(dout, y, pos, w)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rows, pos, dy, dw = step()
+    for seed in (1, 2, 3):
+        q = gen(seed)
+        ids.copy_(torch.stack([torch.randperm(e, generator=q)[:k] for _ in range(t)]).to(torch.int32))
+        dy.fill_(math.nan)
+        graph.replay()
+        torch.cuda.synchronize()
+        behind = rows < 0
+        assert behind.any() and (dy[behind] == 0).all() and torch.isfinite(dy).all()
+        n, named = int((~behind).sum()), pos >= 0
+        want = torch.zeros((n, h), device="cuda")
+        want[pos[named].long()] = (w[..., None] * dout.float()[:, None, :])[named]
+        assert torch.equal(dy[:n], want.bfloat16())
