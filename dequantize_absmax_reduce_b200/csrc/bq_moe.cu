@@ -1018,8 +1018,8 @@ __global__ void __launch_bounds__(128) k_moe_combine_bwd(const CombineBwdArgs a)
 
 // Zeros in the rows of dy that no position names. pair_of is not set up before:
 // where a row is not named it holds anything, but then the pair it tells of, if
-// there is one, has another position. Bound by the rows it writes (30720 of 32768
-// x 7168 bf16: 73 us, 6.0 TB/s); with every row named it reads 8 bytes a row, and
+// there is one, has another position. Bound by the rows it writes (28672 of 32768
+// x 7168 bf16: 73 us, 5.6 TB/s); with every row named it reads 8 bytes a row, and
 // since it starts early costs 1.7 us beside the kernel before it (2049 x 6 x 4096
 // bf16: 39.4 -> 41.1; zeros in all of dy beforehand would write it twice). A warp
 // takes 8 rows.
