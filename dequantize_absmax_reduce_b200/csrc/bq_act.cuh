@@ -53,8 +53,10 @@ __device__ __forceinline__ float act_value(float z) {
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == BQ_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
-    else if constexpr (ACT == BQ_ACT_GELU)
-        return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), 0.5f * (1.0f + erff(z * 0.7071067811865476f)));
+    else if constexpr (ACT == BQ_ACT_GELU) {
+        const float c = clamp_nan(z, 16.0f);
+        return fmaf(c * 0.3989422804014327f, __expf(-0.5f * c * c), 0.5f * (1.0f + erff(c * 0.7071067811865476f)));
+    }
     else if constexpr (ACT == BQ_ACT_GELU_TANH) {
         const float c = clamp_nan(z, 16.0f), s = gelu_gate(c);
         const float q = c * fmaf(c * c, 6.0f * kGeluA * kGeluB, 2.0f * kGeluA);

@@ -213,3 +213,41 @@ def test_combine_backward_of_some_experts_in_a_graph(bq):
         want = torch.zeros((n, h), device="cuda")
         want[pos[named].long()] = (w[..., None] * dout.float()[:, None, :])[named]
         assert torch.equal(dy[:n], want.bfloat16())
+
+
+ACTS = ["none", "relu", "gelu", "gelu_tanh", "silu"]
+
+
+def biases_alone(bq, z, act, out, save_pre=False):
+    """The dense epilogue of a product of zeros: its value before the activation is the bias."""
+    a = torch.zeros((1, 128), dtype=torch.uint8, device="cuda")
+    w = torch.zeros((z.numel(), 128), dtype=torch.uint8, device="cuda")
+    sw = torch.ones(((z.numel() + 127) // 128, 1), device="cuda")
+    return bq.api.fp8_block_gemm_epilogue(a, torch.ones((1, 1), device="cuda"), w, sw, z.cuda(), act, out_dtype=out, save_pre=save_pre)
+
+
+# ---------------------------------------------------------------- slopes at infinity
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("n", [8, 3])
+def test_slope_of_infinite_and_nan_values(bq, act, dtype, n):
+    """The limits of the slopes, 1 and 0, to the last bit; a NaN stays one."""
+    pre = torch.zeros((4, n), dtype=dtype, device="cuda")
+    pre[0], pre[1], pre[2] = math.inf, -math.inf, math.nan
+    dy = torch.full((4, n), 2.0, dtype=dtype, device="cuda")
+    dz, db = bq.api.gemm_epilogue_backward(dy, pre, act)
+    assert (dz[0] == 2).all() and (dz[1] == (2 if act == "none" else 0)).all()
+    assert act == "none" or torch.isnan(dz[2]).all()
+    _, db = bq.api.gemm_epilogue_backward(dy[:2].contiguous(), pre[:2].contiguous(), act)
+    assert (db == (4 if act == "none" else 2)).all()
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_kept_value_past_the_types_range(bq, act):
+    """f16 keeps a value before the activation below -65504 as -inf, after which the activation is 0: so is its gradient."""
+    z = torch.full((64,), -1e5)
+    z[::2] = 1.0
+    c, pre = biases_alone(bq, z, act, HF, True)
+    assert (pre[0, 1::2] == -math.inf).all() and (c[0, 1::2] == 0).all()
+    dz, db = bq.api.gemm_epilogue_backward(torch.ones_like(c), pre, act)
+    assert (dz[0, 1::2] == 0).all() and (db[1::2] == 0).all() and torch.isfinite(dz).all() and torch.isfinite(db).all()
