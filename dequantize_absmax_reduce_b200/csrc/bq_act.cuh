@@ -39,11 +39,42 @@ __device__ __forceinline__ float clamp_nan(float z, float lim) {
     return r;
 }
 
+// The normal distribution's tail for gelu, Phi(-x) at x >= 0, relative to its own
+// size: 1 + erf leaves nothing of gelu below -5.6. Phi(-x) exp(x^2 / 2) falls
+// smoothly from 1/2 to 1 / (x sqrt(2 pi)): it is taken as t times a polynomial of t =
+// 1 / (1 + 0.305 x) whose eight coefficients give the least greatest relative error
+// on [0, 13.5], 1e-7 (a linear program over Chebyshev points); with f32's roundings
+// and the reciprocal's 10 * 2^-24. e = exp(-x^2 / 2), with which it vanishes past
+// 13.2, serves the slope's density too. (Gradient of 4096 x 11008 bf16: 53 us, 75 with
+// erff, 102 with erfcf; 4096 x 18432 x 7168 with bias and kept value: 620, 640, 780.)
+__device__ __forceinline__ float normal_tail(float x, float& e) {
+    float t;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(x, 0.305f, 1.0f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * x * (-0.5f * kLog2e)));
+    float r = fmaf(0.0366991833f, t, -0.152988344f);
+    r = fmaf(r, t, 0.185717046f);
+    r = fmaf(r, t, -0.0379770696f);
+    r = fmaf(r, t, 0.121021859f);
+    r = fmaf(r, t, 0.103420801f);
+    r = fmaf(r, t, 0.122466832f);
+    r = fmaf(r, t, 0.121639736f);
+    return r * t * e;
+}
+// |z|, 16 beyond it (the tail is 0 there, but not times infinity); a NaN stays one.
+__device__ __forceinline__ float tail_arg(float z) {
+    float x;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(fabsf(z)), "f"(16.0f));
+    return x;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
     if constexpr (ACT == BQ_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
-    else if constexpr (ACT == BQ_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
-    else if constexpr (ACT == BQ_ACT_GELU_TANH) return z * gelu_gate(z);
+    else if constexpr (ACT == BQ_ACT_GELU) {                         // max(z, 0) - |z| Phi(-|z|)
+        const float x = tail_arg(z);
+        float e;
+        return fmaf(-x, normal_tail(x, e), fmaxf(z, 0.0f));
+    } else if constexpr (ACT == BQ_ACT_GELU_TANH) return z * gelu_gate(z);
     else if constexpr (ACT == BQ_ACT_SILU) return z * logistic(z);
     else return z;
 }
@@ -54,10 +85,11 @@ template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == BQ_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
     else if constexpr (ACT == BQ_ACT_GELU) {
-        const float c = clamp_nan(z, 16.0f);
-        return fmaf(c * 0.3989422804014327f, __expf(-0.5f * c * c), 0.5f * (1.0f + erff(c * 0.7071067811865476f)));
-    }
-    else if constexpr (ACT == BQ_ACT_GELU_TANH) {
+        const float x = tail_arg(z);
+        float e;
+        const float q = normal_tail(x, e);
+        return fmaf(copysignf(x, z) * 0.3989422804014327f, e, z > 0.0f ? 1.0f - q : q);
+    } else if constexpr (ACT == BQ_ACT_GELU_TANH) {
         const float c = clamp_nan(z, 16.0f), s = gelu_gate(c);
         const float q = c * fmaf(c * c, 6.0f * kGeluA * kGeluB, 2.0f * kGeluA);
         return fmaf(s, fmaf(-s, q, q), s);

@@ -251,3 +251,46 @@ def test_kept_value_past_the_types_range(bq, act):
     assert (pre[0, 1::2] == -math.inf).all() and (c[0, 1::2] == 0).all()
     dz, db = bq.api.gemm_epilogue_backward(torch.ones_like(c), pre, act)
     assert (dz[0, 1::2] == 0).all() and (db[1::2] == 0).all() and torch.isfinite(dz).all() and torch.isfinite(db).all()
+
+
+# ---------------------------------------------------------------- tails of the activations
+def act_and_bound(z, act):
+    """act(z) in 64 bits and the relative error of its f32 evaluation, from the formulas used.
+    An argument's relative error d becomes |x| d of exp(x), and (2 y^2 + 1) d of erfc(y).
+      * gelu, max(z, 0) - |z| Phi(-|z|): the exponent z^2 / 2 has a square, a constant and a product (3 u of it), ex2 within
+        2^-22 (4 u), the factor beside it 10 u, three products: u (1.5 z^2 + 17);
+      * silu, z / (1 + exp(-z)): constant and product of the exponent (2 u |z|), ex2 within 2^-22 (4 u), the sum (1 u), the
+        reciprocal (2 u), the product (1 u): u (2 |z| + 8);
+      * gelu (tanh), the same on the argument 2a: z^2, two constants, a fused step and a product: u (5 |2a| + 8)."""
+    z = z.double()
+    if act == "gelu":
+        return z * 0.5 * torch.erfc(-z / math.sqrt(2.0)), U * (1.5 * z * z + 17)
+    if act == "silu":
+        return z * torch.sigmoid(z), U * (2 * z.abs() + 8)
+    a2 = 2 * math.sqrt(2.0 / math.pi) * (z + 0.044715 * z ** 3)
+    return z * torch.sigmoid(a2), U * (5 * a2.abs() + 8)
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("out", [F32, BF, HF])
+def test_tails_of_the_activations(bq, act, out):
+    """Relative to the value itself, where it is 1e-30 too; what lies below f32's normal numbers may be taken as 0."""
+    z = torch.linspace(-30.0, 10.0, 20000)
+    v, rel = act_and_bound(z, act)
+    got = biases_alone(bq, z, act, out).cpu().double()[0]
+    # Up to 2^-126 of the factor beside z is lost where it leaves the normal numbers.
+    err = rel * (1 + 2.0 ** -10) * v.abs() + 2.0 ** -126 * z.double().abs()
+    bad = (got - v).abs() > err + half_step(v.abs() + err, out)
+    assert not bad.any(), (z[bad][:3], got[bad][:3], v[bad][:3])
+
+
+def test_tail_of_the_gelu_slope(bq):
+    """Phi(z) + z phi(z), relative to the two terms' sizes: Phi as in the forward pass (above 0 from 1, 2 u); phi the same
+    exponential, u (1.5 z^2 + 4), a constant, two products and the last step."""
+    z = torch.linspace(-30.0, 10.0, 20000)
+    d = z.double()
+    big, small = 0.5 * torch.erfc(-d / math.sqrt(2.0)), d * torch.exp(-0.5 * d * d) / math.sqrt(2.0 * math.pi)
+    dz, _ = bq.api.gemm_epilogue_backward(torch.ones((1, z.numel()), device="cuda"), z.cuda()[None], "gelu")
+    bound = U * (big * (1.5 * d * d + 18) + small.abs() * (1.5 * d * d + 8)) * (1 + 2.0 ** -10) + 2.0 ** -126 * (d.abs() + 1)
+    bad = (dz.cpu().double()[0] - (big + small)).abs() > bound
+    assert not bad.any(), (z[bad][:3], dz.cpu()[0][bad][:3], (big + small)[bad][:3])
