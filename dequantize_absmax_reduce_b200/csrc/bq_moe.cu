@@ -471,7 +471,8 @@ __global__ void __launch_bounds__(128, C <= 8 ? 7 : 2) k_moe_route(const RouteAr
 //   softmax, renorm:      dl[id_i] += gs_i s_i (the sum over experts is 0);
 //   softmax as it is:     dl_j = p_j (gs_j - sum_i gs_i s_i) for every expert.
 // Renormalised scores depend on each other's ratios alone, which are taken
-// relative to the largest chosen one, so that small scores do not vanish.
+// relative to the largest chosen one, so that small scores do not vanish (unless
+// f64 holds no score of the row's chosen either, where the weights are 0).
 struct RouteBwdArgs {
     const void* logits;
     const int32_t* ids;
@@ -482,8 +483,13 @@ struct RouteBwdArgs {
     void* dlogits;
 };
 
-template <class T, int C>
-__global__ void __launch_bounds__(128) k_moe_route_bwd(const RouteBwdArgs a) {
+// One kernel for each form: together they would hold each other's registers (5.3 us
+// against 4.7 at 8192 x 128). (Told that four CTAs of the widest rows share an SM, the
+// compiler spends the registers that it has: 4096 x 1024 bf16 sigmoid 9.6 -> 7.6 us.)
+enum RouteForm { ROUTE_SOFTMAX, ROUTE_SHARES, ROUTE_SIGMOID };   // softmax as it is, softmax renormalised, sigmoid
+
+template <class T, int C, RouteForm F>
+__global__ void __launch_bounds__(128, C > 16 ? 4 : 0) k_moe_route_bwd(const RouteBwdArgs a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int64_t t = (int64_t)blockIdx.x * 4 + warp; t < a.tokens; t += (int64_t)gridDim.x * 4) {
         const T* row = reinterpret_cast<const T*>(a.logits) + t * a.experts;
@@ -491,10 +497,11 @@ __global__ void __launch_bounds__(128) k_moe_route_bwd(const RouteBwdArgs a) {
         if (id >= a.experts) id = -1;
         const float g = id >= 0 ? a.dweights[t * a.top_k + lane] : 0.0f;
         const float l = id >= 0 ? ld1<T>(row + id) : -CUDART_INF_F;
-        const bool dense = !a.sigmoid && !a.renorm;
-        float p[C], full[C];
-        float contrib, shift = 0.0f;
-        if (dense) {
+        constexpr bool DENSE = F == ROUTE_SOFTMAX;
+        [[maybe_unused]] float p[C];
+        float full[C], contrib;
+        [[maybe_unused]] float shift = 0.0f;
+        if constexpr (DENSE) {
             load_logits<T, C>(row, lane, a.experts, a.vec, p);
             float top = -CUDART_INF_F;
             bool bad = false;
@@ -517,28 +524,40 @@ __global__ void __launch_bounds__(128) k_moe_route_bwd(const RouteBwdArgs a) {
             shift = warp_sum(contrib * s);
         } else {
             // Scores up to a common factor, and s (1 - s) / s of the sigmoid.
-            const float low = a.sigmoid ? fminf(l, 0.0f) : l;
+            constexpr bool SIGMOID = F == ROUTE_SIGMOID;
+            const bool renorm = !SIGMOID || a.renorm;
+            const float low = SIGMOID ? fminf(l, 0.0f) : l;
             float s = 0.0f, tail = 1.0f;
-            if (a.renorm) {
+            bool none = false;                             // no score left in f64: the weights are 0, not shares
+            if (renorm) {
                 const float top = warp_max(low);
+                if constexpr (SIGMOID) {
+                    none = top < -745.0f;
+                } else {
+                    load_logits<T, C>(row, lane, a.experts, a.vec, p);
+                    float best = top;
+#pragma unroll
+                    for (int i = 0; i < C; ++i) best = fmaxf(best, p[i]);
+                    none = top - warp_max(best) < -745.0f;
+                }
                 s = id >= 0 ? exp_diff(low, top) : 0.0f;
             } else {
                 s = id >= 0 ? expf(low) : 0.0f;
             }
-            if (a.sigmoid) {
+            if constexpr (SIGMOID) {
                 const float u = expf(-fabsf(l));           // s = exp(min(l, 0)) / (1 + u)
                 s = s / (1.0f + u);
                 tail = (l >= 0.0f ? u : 1.0f) / (1.0f + u);   // 1 - s
             }
             float gs;
-            if (a.renorm) {
+            if (renorm) {
                 const float d = warp_sum(s), gm = warp_sum(g * s);
                 s = d > 0.0f ? s / d : 0.0f;
                 gs = a.scale * (g - (d > 0.0f ? gm / d : 0.0f));
             } else {
                 gs = a.scale * g;
             }
-            contrib = id >= 0 ? gs * s * tail : 0.0f;
+            contrib = id >= 0 && !none ? gs * s * tail : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < C; ++i) full[i] = 0.0f;
@@ -549,7 +568,7 @@ __global__ void __launch_bounds__(128) k_moe_route_bwd(const RouteBwdArgs a) {
             for (int i = 0; i < C; ++i)
                 if (lane * C + i == at) full[i] += c;
         }
-        if (dense) {
+        if constexpr (DENSE) {
 #pragma unroll
             for (int i = 0; i < C; ++i) full[i] = p[i] * (full[i] - shift);
         }
@@ -632,11 +651,15 @@ struct RouteBwdLaunch {
     static cudaError_t go(RouteBwdArgs a, cudaStream_t st) {
         constexpr int VEC = Traits<T>::VEC;
         a.vec = a.experts % VEC == 0 && ((uintptr_t)a.logits & 15u) == 0 && ((uintptr_t)a.dlogits & 15u) == 0;
+        return a.sigmoid ? as<ROUTE_SIGMOID>(a, st) : a.renorm ? as<ROUTE_SHARES>(a, st) : as<ROUTE_SOFTMAX>(a, st);
+    }
+    template <RouteForm F>
+    static cudaError_t as(const RouteBwdArgs& a, cudaStream_t st) {
         static int ctas[64] = {0};
         unsigned grid = 0;
-        const cudaError_t e = resident_ctas(k_moe_route_bwd<T, C>, 0, ctas, a.tokens, &grid);
+        const cudaError_t e = resident_ctas(k_moe_route_bwd<T, C, F>, 0, ctas, a.tokens, &grid);
         if (e != cudaSuccess) return e;
-        k_moe_route_bwd<T, C><<<grid, 128, 0, st>>>(a);
+        k_moe_route_bwd<T, C, F><<<grid, 128, 0, st>>>(a);
         return cudaGetLastError();
     }
 };

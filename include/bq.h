@@ -637,7 +637,8 @@ bq_status bq_moe_route(const void* logits, bq_dtype dtype, int64_t tokens, int32
 
 /* Gradient of the weights with respect to the logits (the choice itself and the
  * bias have none): dlogits [tokens, experts] of the logits' dtype, overwritten
- * whole; zero for experts that do not enter a weight. ids as bq_moe_route wrote
+ * whole; zero for experts that do not enter a weight, and for a renormalised row
+ * whose chosen scores are all 0 in f64 (its weights are 0). ids as bq_moe_route wrote
  * them (an id outside [0, experts) has no weight; one that stands twice counts
  * twice), dweights f32 [tokens, top_k]. dlogits must not overlap logits. */
 bq_status bq_moe_route_backward(const void* logits, bq_dtype dtype, int64_t tokens, int32_t experts,

@@ -294,3 +294,30 @@ def test_tail_of_the_gelu_slope(bq):
     bound = U * (big * (1.5 * d * d + 18) + small.abs() * (1.5 * d * d + 8)) * (1 + 2.0 ** -10) + 2.0 ** -126 * (d.abs() + 1)
     bad = (dz.cpu().double()[0] - (big + small)).abs() > bound
     assert not bad.any(), (z[bad][:3], dz.cpu()[0][bad][:3], (big + small)[bad][:3])
+
+
+# ---------------------------------------------------------------- gradients of the weights
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("e", [16, 100, 257])
+def test_gradient_of_scores_that_vanish(bq, dtype, e):
+    """Renormalised scores that 64 bits hold as zeros give weights of 0, whatever the logits: so their gradient is 0."""
+    g = gen(e)
+    bias = torch.zeros(e)
+    bias[5], bias[6] = 11.0, 10.0
+    near = -700.0 if dtype == F32 else -704.0
+    for score, rest in (("sigmoid", -1000.0), ("softmax", 0.0)):
+        x = torch.full((3, e), rest)
+        x[:, 5], x[:, 6] = -900.0, -904.0
+        x[1, 5], x[1, 6] = near, near - 4           # not vanished: shares of 1 / (1 + exp(-4)) and the rest
+        x = x.to(dtype)
+        ids, w = bq.api.moe_route(x.cuda(), 2, bias.cuda(), score)
+        dw = torch.randn((3, 2), generator=g)
+        dx = bq.api.moe_route_backward(x.cuda(), ids, dw.cuda(), score).cpu().double()
+        assert ids.cpu().tolist() == [[5, 6]] * 3 and (w[[0, 2]] == 0).all() and (w[1] > 0).all()
+        assert (dx[[0, 2]] == 0).all()
+        r = 1 / (1 + math.exp(-4.0))
+        ref = r * (1 - r) * (dw[1, 0] - dw[1, 1]).double()
+        # g - sum and its product, 2^-18 of s (|g| + sum |g s|) as for every such gradient, and the result's half step
+        size = r * 2 * dw[1].abs().sum().double()
+        for at, want in ((5, ref), (6, -ref)):
+            assert (dx[1, at] - want).abs() <= 2.0 ** -18 * size + half_step(want, dtype)
