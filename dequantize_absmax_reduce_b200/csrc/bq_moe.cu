@@ -91,6 +91,14 @@ __device__ __forceinline__ float exp_diff(float a, float b) {
     const float e = expf(d);
     return fmaf(e, lost, e);
 }
+// The same for a share of which a result in T is made: for 16 bits the difference's
+// rounding (at most 2^-18 of the share before exp leaves f32's normal numbers) is far
+// below half a step.
+template <class T>
+__device__ __forceinline__ float exp_share(float a, float b) {
+    if constexpr (std::is_same<T, float>::value) return exp_diff(a, b);
+    else return expf(a == b ? 0.0f : a - b);
+}
 // Integers in the order of floats; above 0, which stands for "not available".
 __device__ __forceinline__ uint32_t order_key(float v) {
     const uint32_t b = __float_as_uint(v);
@@ -511,7 +519,7 @@ __global__ void __launch_bounds__(128, C > 16 ? 4 : 0) k_moe_route_bwd(const Rou
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                p[i] = lane * C + i < a.experts ? expf(p[i] == top ? 0.0f : p[i] - top) : 0.0f;
+                p[i] = lane * C + i < a.experts ? exp_share<T>(p[i], top) : 0.0f;
                 sum += p[i];
             }
             sum = warp_sum(sum);
@@ -519,7 +527,7 @@ __global__ void __launch_bounds__(128, C > 16 ? 4 : 0) k_moe_route_bwd(const Rou
             const float inv = 1.0f / sum;
 #pragma unroll
             for (int i = 0; i < C; ++i) p[i] *= inv;
-            const float s = id >= 0 ? expf(l == top ? 0.0f : l - top) * inv : 0.0f;
+            const float s = id >= 0 ? exp_share<T>(l, top) * inv : 0.0f;
             contrib = a.scale * g;
             shift = warp_sum(contrib * s);
         } else {

@@ -321,3 +321,20 @@ def test_gradient_of_scores_that_vanish(bq, dtype, e):
         size = r * 2 * dw[1].abs().sum().double()
         for at, want in ((5, ref), (6, -ref)):
             assert (dx[1, at] - want).abs() <= 2.0 ** -18 * size + half_step(want, dtype)
+
+
+def test_dense_gradient_of_small_shares(bq):
+    """Softmax as it is, chosen logits 60 to 87 below the largest: relative to their size. An exponential within 2 ulp (4 u)
+    and its argument's rounding given back (1 u), the sum of 256 (8 u), reciprocal, and five products and sums: below 2^-19."""
+    g = gen(61)
+    x = -60.0 - 27.0 * torch.rand((400, 256), generator=g)
+    x[:, 17] = torch.rand(400, generator=g)
+    ids = torch.stack([torch.randperm(256, generator=g)[:6] for _ in range(400)]).to(torch.int32)
+    dw = torch.randn((400, 6), generator=g)
+    dx = bq.api.moe_route_backward(x.cuda(), ids.cuda(), dw.cuda(), "softmax", False).cpu().double()
+    p = torch.softmax(x.double(), -1)
+    full = torch.zeros_like(p).scatter_add_(1, ids.long(), dw.double())
+    shift = (p * full).sum(-1, keepdim=True)
+    size = p * (full.abs() + (p * full.abs()).sum(-1, keepdim=True))
+    # (products with what is left of p below f32's normal numbers: 2^-149 a step, a few of them)
+    assert ((dx - p * (full - shift)).abs() <= 2.0 ** -19 * size + 2.0 ** -146).all()
