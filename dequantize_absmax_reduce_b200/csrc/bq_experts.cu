@@ -137,17 +137,6 @@ __device__ __forceinline__ Tile tile_at(const ExpertArgs& g, const volatile int*
     return t;
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_regs_ready16(uint32_t (&r)[16]) {
-    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                      "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
-}
 __device__ __forceinline__ uint32_t cluster_size() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
@@ -169,16 +158,7 @@ __device__ __forceinline__ void add_scaled(F2 (&acc)[M], const uint32_t (&r)[N],
 // own scale.
 template <int SW>
 __device__ __forceinline__ void promote_runs(F2 (&acc)[SW], uint32_t t0, uint32_t t1, F2 c0, F2 c1) {
-    if constexpr (SW == 16) {
-        uint32_t r0[16], r1[16];
-        tmem_ld16(t0, r0);
-        tmem_ld16(t1, r1);
-        tmem_ld_wait();
-        tmem_regs_ready16(r0);
-        tmem_regs_ready16(r1);
-        add_scaled<16, 0>(acc, r0, c0);
-        add_scaled<16, 8>(acc, r1, c1);
-    } else if constexpr (SW == 32) {
+    if constexpr (SW == 32) {
         uint32_t r0[32], r1[32];
         tmem_ld32(t0, r0);
         tmem_ld32(t1, r1);
