@@ -47,7 +47,7 @@ static_assert(128 * REGX_CTL + 256 * REGX_ACC <= X_NT * REGX_LAUNCH, "register s
 // XR: rows of a tile. The MMA always takes 128; behind a tile of 32 a slot holds
 // zeros. Slots of 32 rows, with other slots' bytes behind them, leave the ring a
 // fourth stage, but products that nobody reads cost clock at the power limit (64
-// rows on 32 experts of 4096 x 7168, call after call: 173 us against 163).
+// rows on 32 experts of 4096 x 7168, call after call at that limit: 173 us against 163).
 template <int BN, int XR>
 struct PlanX {
     // k-blocks of a ring stage and of a TMEM buffer: each signal between the
@@ -622,25 +622,34 @@ cudaError_t launch_experts(const uint8_t* w, const ExpertArgs& ga, cudaStream_t 
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Tile shapes, by how many rows an expert has on average and how many tiles
-// there are (times on B200, us a product of 32 experts n 4096 k 7168 gated unless said):
-//   256 columns from 128 rows an expert on (16384 rows: 686 against 766 with 128
-//   columns; 4096: 232 against 248; 62 rows an expert of n 7168 k 2048: 128.5
-//   against 121), with tiles enough to fill the card twice;
-//   tiles of 32 rows up to 8 rows an expert (64 rows: 140 against 150; 256: 155
-//   against 162; 16 rows an expert of n 7168 k 2048: 120 against 117).
+// Tile shapes, by whether rows are gathered, how many an expert has on average and
+// how many tiles there are. Times on B200 in us, launches of a CUDA graph call
+// after call; 32 experts, n 4096 k 7168 gated ("up") or n 7168 k 2048 ("down"):
+//   rows gathered, up to 16 an expert: tiles of 32 rows x 128 columns (up, 64 rows:
+//   151 against 207 with 128 rows and 158 with 256 columns; 256: 161, 208, 163; 512:
+//   174, 209, 167; one expert, 128 rows: 21, 35, 34);
+//   rows gathered, more of them: 256 columns (up, 768 rows: 173 against 190 with 32
+//   rows and 210 with 128 x 128; 16384: 597 against 952; 8 experts of 2048 x 2048, 512
+//   rows: 16.2 against 15.8). The 128 columns' two k-blocks a stage wait for their
+//   gather;
+//   rows in place: 256 columns from 16 rows an expert on (down, 512 rows: 103 against
+//   110 with 128 columns, 4096: 137 against 149; up, 512: 166 either way, 4096: 212
+//   against 234), with tiles enough to fill the card twice (8 experts of 2048 x 1024,
+//   512 rows: 13.3 against 10.3), else 128 (down, 64 rows: 93 against 97, and 100 with
+//   tiles of 32 rows; up, 64: 150, 154, 150).
 //   Widths that are no multiple of 8 stay on 128 columns, whose promotion leaves
 //   room for their epilogue.
 template <bool GATED>
 cudaError_t launch_by_shape(const uint8_t* w, const ExpertArgs& g, cudaStream_t st) {
     const int64_t p = g.p, e = g.n_experts;
+    const bool few = g.rows && p <= 16 * e;
     if constexpr (!GATED) {
         if (g.n % 8 != 0)
-            return p <= 8 * e ? launch_experts<128, false, 32, false, true>(w, g, st)
-                              : launch_experts<128, false, 128, false, true>(w, g, st);
+            return few ? launch_experts<128, false, 32, false, true>(w, g, st) : launch_experts<128, false, 128, false, true>(w, g, st);
     }
-    if (p <= 8 * e) return launch_experts<128, GATED, 32, false, false>(w, g, st);
-    if (p >= 128 * e && (p / XM) * ((g.n + 255) / 256) >= 2 * sm_count())
+    if (few) return launch_experts<128, GATED, 32, false, false>(w, g, st);
+    const int64_t row_tiles = max(p / XM, min(p, e));            // about
+    if (g.rows || (p >= 16 * e && row_tiles * ((g.n + 255) / 256) >= 2 * sm_count()))
         return launch_experts<256, GATED, 128, false, false>(w, g, st);
     return launch_experts<128, GATED, 128, false, false>(w, g, st);
 }
