@@ -135,7 +135,7 @@ lib.bq_packed_transpose_stride.argtypes = [_I64, _I64]
 lib.bq_packed_transpose_stride.restype = _I64
 lib.bq_gemm_epilogue_backward_workspace_size.argtypes = [_I64, _I64]
 lib.bq_gemm_epilogue_backward_workspace_size.restype = _SZ
-lib.bq_moe_combine_backward_workspace_size.argtypes = [_I64]
+lib.bq_moe_combine_backward_workspace_size.argtypes = [_I64, _I64, _I32]
 lib.bq_moe_combine_backward_workspace_size.restype = _SZ
 lib.bq_check_device_error.argtypes = []
 lib.bq_check_device_error.restype = C.c_int
@@ -632,11 +632,11 @@ def bq_moe_combine_backward(dout, y, pos, weights, dy, dweights, stream=None):
     _combine_backward("bq_moe_combine_backward", dout, y, pos, weights, dy, dweights, stream)
 
 
-def bq_moe_combine_backward_workspace_size(y_rows: int) -> int:
-    return int(lib.bq_moe_combine_backward_workspace_size(y_rows))
+def bq_moe_combine_backward_workspace_size(y_rows: int, tokens: int, top_k: int) -> int:
+    return lib.bq_moe_combine_backward_workspace_size(y_rows, tokens, top_k)
 
 
-def bq_moe_combine_backward_whole(dout, y, pos, weights, dy, dweights, ws, stream=None):
+def bq_moe_combine_backward_whole(dout, y, pos, weights, dy, dweights, ws=None, stream=None):
     ws_at = _need(ws, "ws", (0 if ws is None else ws.numel(),), _U8T, y.get_device())
     _combine_backward("bq_moe_combine_backward_whole", dout, y, pos, weights, dy, dweights, stream, ws_at, _nbytes(ws))
 

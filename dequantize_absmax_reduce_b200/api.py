@@ -459,8 +459,10 @@ def moe_combine_backward(dout, y, pos, weights, stream=None):
     position names are zeros."""
     dy = torch.empty_like(y)
     dw = torch.empty_like(weights)
-    with _scratch_of(stream, y):
-        ws = torch.empty(B.bq_moe_combine_backward_workspace_size(y.shape[0]), dtype=torch.uint8, device=y.device)
+    ws, size = None, B.bq_moe_combine_backward_workspace_size(y.shape[0], *pos.shape)
+    if size:
+        with _scratch_of(stream, y):
+            ws = torch.empty(size, dtype=torch.uint8, device=y.device)
     B.bq_moe_combine_backward_whole(dout, y, pos, weights, dy, dw, ws, stream)
     return dy, dw
 

@@ -969,7 +969,24 @@ struct CombineBwdArgs {
     int32_t* pair_of;          // [y_rows] or null: the pair (token, slot) that names each row, for k_zero_unnamed
     int64_t tokens, y_rows, hidden;
     int top_k;
+    int slice;                 // rows that each CTA looks over for names and zeroes, or 0
 };
+// Few enough pairs that every CTA can look through all of them for the names of its
+// share of the rows, and the rows of a share at most.
+constexpr int FEW_PAIRS = 2048, FEW_ROWS = 2048;
+bool few_named(int64_t y_rows, int64_t pairs) { return y_rows <= FEW_ROWS && pairs <= FEW_PAIRS; }
+
+// Zeros in a row of dy (its start and size in bytes), by nt threads.
+__device__ __forceinline__ void zero_row(uint8_t* row, int64_t bytes, bool wide, int tid, int nt) {
+    if (wide) {
+        for (int64_t i = tid * 16; i < bytes; i += nt * 16) st16(row + i, U4{0u, 0u, 0u, 0u});
+    } else {
+        for (int64_t i = tid * 2; i < bytes; i += nt * 2) *reinterpret_cast<uint16_t*>(row + i) = 0;
+    }
+}
+__device__ __forceinline__ bool rows_wide(const void* dy, int64_t row_bytes) {
+    return row_bytes % 16 == 0 && ((uintptr_t)dy & 15u) == 0;
+}
 
 template <class T, int W, int U>
 __global__ void __launch_bounds__(128) k_moe_combine_bwd(const CombineBwdArgs a) {
@@ -1045,19 +1062,37 @@ __global__ void __launch_bounds__(128) k_moe_combine_bwd(const CombineBwdArgs a)
         __syncthreads();
     }
     pdl_trigger();
+    if (a.slice) {
+        __shared__ uint32_t named[FEW_ROWS / 32];
+        const int lo = blockIdx.x * a.slice, hi = min((int)a.y_rows, lo + a.slice), pairs = (int)a.tokens * a.top_k;
+        const int64_t row_bytes = a.hidden * (int64_t)sizeof(T);
+        const bool wide = rows_wide(a.dy, row_bytes);
+        if (threadIdx.x < FEW_ROWS / 32) named[threadIdx.x] = 0u;
+        __syncthreads();
+        for (int i = threadIdx.x; i < pairs; i += 128) {
+            const int p = __ldg(a.pos + i);
+            if (p >= lo && p < hi) atomicOr(&named[(p - lo) >> 5], 1u << ((p - lo) & 31));
+        }
+        __syncthreads();
+        for (int r = lo; r < hi; ++r)
+            if (!((named[(r - lo) >> 5] >> ((r - lo) & 31)) & 1u))
+                zero_row(reinterpret_cast<uint8_t*>(a.dy) + r * row_bytes, row_bytes, wide, threadIdx.x, 128);
+    }
 }
 
-// Zeros in the rows of dy that no position names. pair_of is not set up before:
-// where a row is not named it holds anything, but then the pair it tells of, if
-// there is one, has another position. Bound by the rows it writes (28672 of 32768
-// x 7168 bf16: 73 us, 5.6 TB/s); with every row named it reads 8 bytes a row, and
-// since it starts early costs 1.7 us beside the kernel before it (2049 x 6 x 4096
-// bf16: 39.4 -> 41.1; zeros in all of dy beforehand would write it twice). A warp
-// takes 8 rows.
+// Zeros in the rows of dy that no position names, where the kernel above does not
+// look them over itself (with few pairs it does: one launch and no scratch). pair_of
+// is not set up before: where a row is not named it holds anything, but then the pair
+// it tells of, if there is one, has another position. Bound by the rows it writes
+// (28672 of 32768 x 7168 bf16: 73 us, 5.6 TB/s); with every row named it reads 8
+// bytes a row, and since it starts early costs 1.7 us behind the kernel before it
+// (both 39.4 us at 2049 x 6 x 4096 bf16; zeros in all of dy beforehand would write it
+// twice). A warp takes 8 rows.
 __global__ void __launch_bounds__(128) k_zero_unnamed(const int32_t* pair_of, const int32_t* pos, int pairs, int64_t rows,
-                                                      int64_t row_bytes, int wide, uint8_t* dy) {
+                                                      int64_t row_bytes, uint8_t* dy) {
     pdl_wait();
     const int lane = threadIdx.x & 31;
+    const bool wide = rows_wide(dy, row_bytes);
     for (int64_t r0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 5)) * 8; r0 < rows; r0 += (int64_t)gridDim.x * 32) {
         const int64_t r = r0 + lane;
         bool bare = false;
@@ -1066,12 +1101,7 @@ __global__ void __launch_bounds__(128) k_zero_unnamed(const int32_t* pair_of, co
             bare = pair < 0 || pair >= pairs || pos[pair] != r;
         }
         for (unsigned todo = __ballot_sync(FULL, bare); todo; todo &= todo - 1) {
-            uint8_t* row = dy + (r0 + __ffs(todo) - 1) * row_bytes;
-            if (wide) {
-                for (int64_t i = lane * 16; i < row_bytes; i += 512) st16(row + i, U4{0u, 0u, 0u, 0u});
-            } else {
-                for (int64_t i = lane * 2; i < row_bytes; i += 64) *reinterpret_cast<uint16_t*>(row + i) = 0;
-            }
+            zero_row(dy + (r0 + __ffs(todo) - 1) * row_bytes, row_bytes, wide, lane, 32);
         }
     }
 }
@@ -1110,9 +1140,11 @@ cudaError_t combine_out(const CombineArgs& a, bq_dtype out, cudaStream_t st) {
     return launch_combine<TY, __nv_bfloat16>(a, st);
 }
 template <class T>
-cudaError_t launch_combine_bwd(const CombineBwdArgs& a, cudaStream_t st) {
-    const int64_t most = (int64_t)sm_count() * 16;
-    const unsigned grid = (unsigned)(a.tokens < most ? a.tokens : most);
+cudaError_t launch_combine_bwd(CombineBwdArgs a, bool look_over, cudaStream_t st) {
+    const int64_t most = (int64_t)sm_count() * 16, share = look_over ? (a.y_rows + 7) / 8 : 0;   // (8 rows a CTA)
+    const int64_t want = a.tokens > share ? a.tokens : share;
+    const unsigned grid = (unsigned)(want < most ? want : most);
+    a.slice = look_over ? (int)((a.y_rows + grid - 1) / grid) : 0;
     switch (col_width(a.hidden, (uintptr_t)a.dout | (uintptr_t)a.y | (uintptr_t)a.dy, sizeof(T))) {
         case 8: k_moe_combine_bwd<T, 8, 1><<<grid, 128, 0, st>>>(a); break;
         case 2: k_moe_combine_bwd<T, 2, 4><<<grid, 128, 0, st>>>(a); break;
@@ -1122,12 +1154,12 @@ cudaError_t launch_combine_bwd(const CombineBwdArgs& a, cudaStream_t st) {
 }
 cudaError_t launch_zero_unnamed(const CombineBwdArgs& a, size_t es, cudaStream_t st) {
     const int64_t row_bytes = a.hidden * (int64_t)es, need = (a.y_rows + 31) / 32, most = 16ll * sm_count();
-    const int wide = row_bytes % 16 == 0 && ((uintptr_t)a.dy & 15u) == 0, pairs = (int)(a.tokens * a.top_k);
+    const int pairs = (int)(a.tokens * a.top_k);
     const unsigned grid = (unsigned)(need < most ? need : most);
     if (pairs > 0)
-        return launch_pdl(k_zero_unnamed, grid, 128, 0, st, (const int32_t*)a.pair_of, a.pos, pairs, a.y_rows, row_bytes, wide,
+        return launch_pdl(k_zero_unnamed, grid, 128, 0, st, (const int32_t*)a.pair_of, a.pos, pairs, a.y_rows, row_bytes,
                           (uint8_t*)a.dy);
-    k_zero_unnamed<<<grid, 128, 0, st>>>(a.pair_of, a.pos, pairs, a.y_rows, row_bytes, wide, (uint8_t*)a.dy);
+    k_zero_unnamed<<<grid, 128, 0, st>>>(a.pair_of, a.pos, pairs, a.y_rows, row_bytes, (uint8_t*)a.dy);
     return cudaGetLastError();
 }
 
@@ -1229,19 +1261,21 @@ static bq_status combine_backward(const void* dout, const void* y, bq_dtype dtyp
     if (tokens > 0 && ((!dout && hidden > 0) || (!y && y_rows > 0 && hidden > 0) || !pos || !weights || !dweights))
         return BQ_ERR_INVALID_ARG;
     if (!dy && y_rows > 0 && hidden > 0) return BQ_ERR_INVALID_ARG;
-    if (zeros && tokens > 0 && (!ws || ws_bytes < bq_moe_combine_backward_workspace_size(y_rows))) return BQ_ERR_INVALID_ARG;
+    const size_t scratch = zeros ? bq_moe_combine_backward_workspace_size(y_rows, tokens, top_k) : 0;
+    if (scratch > 0 && (!ws || ws_bytes < scratch)) return BQ_ERR_INVALID_ARG;
     const uintptr_t m = type_mask(dtype);
     if (misaligned(dout, m) || misaligned(y, m) || misaligned(dy, m) || misaligned(pos, 3) || misaligned(weights, 3) ||
         misaligned(dweights, 3) || misaligned(ws, 3))
         return BQ_ERR_MISALIGNED;
-    CombineBwdArgs a{dout, y, pos, weights, dy, dweights, zeros ? (int32_t*)ws : nullptr, tokens, y_rows, hidden, top_k};
+    CombineBwdArgs a{dout, y, pos, weights, dy, dweights, scratch > 0 ? (int32_t*)ws : nullptr, tokens, y_rows, hidden, top_k, 0};
     cudaStream_t st = (cudaStream_t)stream;
+    const bool few = zeros && few_named(y_rows, tokens * top_k);
     cudaError_t e = cudaSuccess;
-    if (tokens > 0)
-        e = dtype == BQ_F32 ? launch_combine_bwd<float>(a, st)
-            : dtype == BQ_F16 ? launch_combine_bwd<__half>(a, st)
-                              : launch_combine_bwd<__nv_bfloat16>(a, st);
-    if (e == cudaSuccess && zeros) e = launch_zero_unnamed(a, dtype == BQ_F32 ? 4 : 2, st);
+    if (tokens > 0 || few)
+        e = dtype == BQ_F32 ? launch_combine_bwd<float>(a, few, st)
+            : dtype == BQ_F16 ? launch_combine_bwd<__half>(a, few, st)
+                              : launch_combine_bwd<__nv_bfloat16>(a, few, st);
+    if (e == cudaSuccess && zeros && !few) e = launch_zero_unnamed(a, dtype == BQ_F32 ? 4 : 2, st);
     return from(e);
 }
 
@@ -1251,8 +1285,9 @@ extern "C" bq_status bq_moe_combine_backward(const void* dout, const void* y, bq
     return combine_backward(dout, y, dtype, y_rows, hidden, pos, weights, tokens, top_k, dy, dweights, false, nullptr, 0, stream);
 }
 
-extern "C" size_t bq_moe_combine_backward_workspace_size(int64_t y_rows) {
-    return y_rows > 0 && y_rows < (1ll << 31) ? (size_t)y_rows * sizeof(int32_t) : 0;
+extern "C" size_t bq_moe_combine_backward_workspace_size(int64_t y_rows, int64_t tokens, int32_t top_k) {
+    if (y_rows <= 0 || y_rows >= (1ll << 31) || tokens <= 0 || top_k < 1 || !pairs_fit(tokens, top_k)) return 0;
+    return few_named(y_rows, tokens * top_k) ? 0 : (size_t)y_rows * sizeof(int32_t);
 }
 
 extern "C" bq_status bq_moe_combine_backward_whole(const void* dout, const void* y, bq_dtype dtype, int64_t y_rows,

@@ -676,10 +676,11 @@ bq_status bq_moe_combine_backward(const void* dout, const void* y, bq_dtype dtyp
                                   int64_t hidden, const int32_t* pos, const float* weights,
                                   int64_t tokens, int32_t top_k, void* dy, float* dweights,
                                   void* stream);
-/* The same with zeros in the rows of dy that no pos names (two launches). ws:
- * scratch of bq_moe_combine_backward_workspace_size(y_rows) bytes (device,
- * 4-byte aligned; its contents do not matter), y_rows < 2^31. */
-size_t bq_moe_combine_backward_workspace_size(int64_t y_rows);
+/* The same with zeros in the rows of dy that no pos names. ws: scratch of
+ * bq_moe_combine_backward_workspace_size(y_rows, tokens, top_k) bytes (device,
+ * 4-byte aligned; its contents do not matter), NULL where that is 0, as it is for
+ * up to 2048 rows and pairs; those take one launch, others two. y_rows < 2^31. */
+size_t bq_moe_combine_backward_workspace_size(int64_t y_rows, int64_t tokens, int32_t top_k);
 bq_status bq_moe_combine_backward_whole(const void* dout, const void* y, bq_dtype dtype, int64_t y_rows,
                                         int64_t hidden, const int32_t* pos, const float* weights,
                                         int64_t tokens, int32_t top_k, void* dy, float* dweights,

@@ -155,7 +155,7 @@ def half_step(t, dtype):
 # ---------------------------------------------------------------- gradient rows that nobody names
 @pytest.mark.parametrize("dtype", [BF, HF, F32])
 @pytest.mark.parametrize("t,k,h,p", [(1, 1, 1, 5), (5, 3, 7, 40), (33, 6, 1000, 500), (64, 8, 4096, 700), (9, 32, 136, 288), (0, 4, 64, 37),
-                                     (6, 2, 9001, 100), (20, 2, 66, 3000)])
+                                     (6, 2, 9001, 100), (20, 2, 66, 3000), (700, 4, 24, 2900), (512, 4, 40, 2048), (513, 4, 40, 2052), (0, 3, 40, 2500)])
 @pytest.mark.parametrize("stream", [None, "other", "raw"])
 def test_combine_backward_returns_no_unwritten_row(bq, dtype, t, k, h, p, stream):
     """Rows of the returned gradient that no position names are zeros: memory that held NaN before is handed out."""

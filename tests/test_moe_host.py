@@ -149,15 +149,16 @@ def test_route_group_values(B):
 
 
 def test_combine_backward_whole_refusals(B):
-    """As bq_moe_combine_backward, and its scratch."""
-    f = lambda d=P, y=P, dt=B.BQ_F16, yr=8, h=16, pos=P, w=P, t=4, k=2, dy=P, dw=P, ws=P, wb=32: B.lib.bq_moe_combine_backward_whole(   # noqa: E731
-        d, y, dt, yr, h, pos, w, t, k, dy, dw, ws, wb, None)
+    """As bq_moe_combine_backward, and its scratch (none for few rows and pairs)."""
+    f = lambda d=P, y=P, dt=B.BQ_F16, yr=3000, h=16, pos=P, w=P, t=4, k=2, dy=P, dw=P, ws=P, wb=12000: (   # noqa: E731
+        B.lib.bq_moe_combine_backward_whole(d, y, dt, yr, h, pos, w, t, k, dy, dw, ws, wb, None))
     assert f(dt=B.BQ_F64) == B.BQ_ERR_UNSUPPORTED
     for kw in ({"yr": -1}, {"yr": 1 << 31}, {"h": -1}, {"t": -1}, {"k": 0}, {"k": 33}, {"d": None}, {"y": None}, {"pos": None}, {"w": None},
-               {"dy": None}, {"dw": None}, {"ws": None}, {"wb": 31}, {"t": 0, "dy": None}):
+               {"dy": None}, {"dw": None}, {"ws": None}, {"wb": 11999}, {"t": 0, "dy": None}, {"yr": 8, "ws": None, "dy": None}):
         assert f(**kw) == B.BQ_ERR_INVALID_ARG, kw
     for kw in ({"d": P + 1}, {"y": P + 1}, {"dy": P + 1}, {"pos": P + 1}, {"w": P + 2}, {"dw": P + 2}, {"ws": P + 2}):
         assert f(**kw) == B.BQ_ERR_MISALIGNED, kw
     assert f(t=0, yr=0) == B.BQ_OK and f(t=0, h=0) == B.BQ_OK
-    ws = B.bq_moe_combine_backward_workspace_size
-    assert ws(8) == 32 and ws(0) == 0 and ws(-1) == 0 and ws(1 << 31) == 0
+    size = B.bq_moe_combine_backward_workspace_size
+    assert size(2048, 256, 8) == 0 and size(2049, 256, 8) == 8196 and size(8, 2049, 1) == 32
+    assert size(0, 4, 2) == 0 and size(-1, 4, 2) == 0 and size(1 << 31, 4, 2) == 0 and size(3000, 0, 2) == 0 and size(3000, 4, 0) == 0
