@@ -338,3 +338,41 @@ def test_dense_gradient_of_small_shares(bq):
     size = p * (full.abs() + (p * full.abs()).sum(-1, keepdim=True))
     # (products with what is left of p below f32's normal numbers: 2^-149 a step, a few of them)
     assert ((dx - p * (full - shift)).abs() <= 2.0 ** -19 * size + 2.0 ** -146).all()
+
+
+# ---------------------------------------------------------------- gathered rows on wide tiles
+@pytest.mark.parametrize("counts", [[40], [17, 0, 130, 1, 90], [200, 129]])
+@pytest.mark.parametrize("n,k", [(8, 128), (64, 384), (136, 1152), (512, 640)])
+def test_grouped_gathered_rows_on_wide_tiles(bq, counts, n, k):
+    """More than 16 gathered rows an expert, narrow and few weights, scales off 16-byte boundaries, rows outside the
+    activations, positions behind the last: the sums are those of the dense product of each expert's rows, where one CTA
+    sums all of k (bit for bit: the same blocks in the same order), and the same every time."""
+    g = gen(n + k + sum(counts))
+    e, p, t = len(counts), sum(counts), 70
+
+    def codes(*shape):
+        c = torch.randint(0, 256, shape, generator=g, dtype=torch.uint8)
+        return torch.where((c & 127) == 127, 0x38, c).to(torch.uint8).cuda()
+    off16 = lambda v: torch.cat([v.new_zeros(1), v.reshape(-1)])[1:].view(v.shape)   # noqa: E731
+    a, sa = codes(t, k), off16((torch.rand((t, k // 128), generator=g) * 0.01).cuda())
+    w, sw = codes(e, n, k), off16((torch.rand((e, (n + 127) // 128, k // 128), generator=g) * 0.01).cuda())
+    rows = torch.randint(0, t, (p + 5,), generator=g).to(torch.int32)
+    rows[3], rows[9] = -1, t
+    at = [0]
+    for c in counts:
+        at.append(at[-1] + c)
+    offsets = torch.tensor(at, dtype=torch.int32, device="cuda")
+    out = torch.full((p + 5, n), 3.0, device="cuda")
+    for _ in range(3):
+        bq.api.fp8_grouped_gemm(a, sa, offsets, w, sw, rows.cuda(), act="silu", out=out)
+        assert (out[p:] == 3.0).all() and (out[[3, 9]] == 0).all()
+        for i in range(e):
+            mine = rows[at[i]:at[i + 1]].long()
+            here = (mine >= 0) & (mine < t)
+            if not here.any():
+                continue
+            x = mine[here].cuda()
+            z = bq.api.fp8_block_gemm_quantized(a[x], sa[x], w[i], sw[i].clone(), F32)
+            got = out[at[i]:at[i + 1]][here.cuda()].double()
+            want, rel = act_and_bound(z, "silu")
+            assert ((got - want).abs() <= rel * want.abs() + half_step(want, F32) + 2.0 ** -126 * z.double().abs()).all()
