@@ -53,9 +53,9 @@ TRAFFIC_SOURCES = ("bq_abi.cu", "bq_int.cu", "bq_pipe.cu", "bq_pipe_bf16.cu", "b
                    "bq_pipe_args.h", "bq_device.cuh", "bq_internal.h", "bq_map_ops.cuh",
                    "bq_quant_ops.cuh", "bq_range.cuh")
 NCU_TRAFFIC = {
-    "quantize_per_token": {"src_sha256": "904bee8c921e0bedfe55107f1007f3ceaadd5fefdc7ba33a732fee7952293eba", "bytes_per_launch": 70573056},
-    "dequantize_per_token": {"src_sha256": "904bee8c921e0bedfe55107f1007f3ceaadd5fefdc7ba33a732fee7952293eba", "bytes_per_launch": 39866624},
-    "quantize_per_token_backward": {"src_sha256": "904bee8c921e0bedfe55107f1007f3ceaadd5fefdc7ba33a732fee7952293eba", "bytes_per_launch": 159505152},
+    "quantize_per_token": {"src_sha256": "6234404c348891d9f6c46f2b09f7822a9e8bd35f6c681e365cdf9804a6172eb0", "bytes_per_launch": 70078976},
+    "dequantize_per_token": {"src_sha256": "6234404c348891d9f6c46f2b09f7822a9e8bd35f6c681e365cdf9804a6172eb0", "bytes_per_launch": 38849536},
+    "quantize_per_token_backward": {"src_sha256": "6234404c348891d9f6c46f2b09f7822a9e8bd35f6c681e365cdf9804a6172eb0", "bytes_per_launch": 159147520},
 }
 
 

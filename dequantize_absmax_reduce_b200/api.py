@@ -459,7 +459,8 @@ def moe_combine_backward(dout, y, pos, weights, stream=None):
     position names are zeros."""
     dy = torch.empty_like(y)
     dw = torch.empty_like(weights)
-    ws, size = None, B.bq_moe_combine_backward_workspace_size(y.shape[0], *pos.shape)
+    t, top_k = pos.shape
+    ws, size = None, B.bq_moe_combine_backward_workspace_size(y.shape[0], t, top_k)
     if size:
         with _scratch_of(stream, y):
             ws = torch.empty(size, dtype=torch.uint8, device=y.device)
